@@ -1,6 +1,7 @@
 /*
  * libscan.h -- device-wide parallel prefix primitives over 32-bit integers
- * for AMD Instinct MI355X (gfx950).  C ABI.
+ * for AMD Instinct MI355X (gfx950), and the scans that language models run on
+ * them: linear attention with decay and token sampling.  C ABI.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -53,7 +54,7 @@ enum {
     LIBSCAN_ERR_ARG = -3,      /* an argument outside its documented range */
     LIBSCAN_ERR_SCRATCH = -4,  /* scratch_bytes below the size query's answer */
     LIBSCAN_ERR_HIP = -5,      /* a HIP runtime call failed */
-    LIBSCAN_ERR_ALIGN = -6     /* a pointer is not 4-byte aligned */
+    LIBSCAN_ERR_ALIGN = -6     /* a pointer is not aligned to its elements */
 };
 
 /* Largest n accepted by the scans and the segmented scan (2^36 elements,
@@ -397,6 +398,161 @@ int compact_flags_u32(const int32_t *flags, int32_t *out_idx, uint64_t n, uint32
 size_t radix_scratch_bytes(uint64_t n, int bits_per_pass);
 int radix_perm_u32(const uint32_t *keys, int32_t *perm, uint64_t n, int bits_per_pass,
                    void *scratch, size_t scratch_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Linear attention with a decay for each head                              */
+/* ------------------------------------------------------------------------ */
+
+/* Element types of the rows (states are always floats). */
+enum { LIBSCAN_F32 = 0, LIBSCAN_BF16 = 1, LIBSCAN_F16 = 2 };
+
+/* Largest key_width and value_width. */
+#define LINATTN_MAX_WIDTH 128
+
+/*
+ * Rows of one tensor: token t of sequence s, head h starts `s * seq_stride +
+ * t * token_stride + h * head_stride` ELEMENTS after data; the elements of a
+ * row are contiguous.  An input may have fewer heads than the operator: the
+ * number must divide the operator's, and head h then reads head
+ * h / (heads of the operator / heads of the input).  data is aligned to its
+ * element; rows that all start on 16 bytes and are whole multiples of them
+ * move with 16-byte accesses.
+ */
+typedef struct {
+    void *data;
+    int64_t seq_stride, token_stride, head_stride;
+    uint32_t heads;
+} linattn_rows_t;
+
+/*
+ * ends NULL: `seqs` sequences of `tokens` tokens each.  Else device, `seqs`
+ * u32 (what runs_layout_u32 leaves): the sequences lie one after another in
+ * `tokens` rows, sequence s at tokens [ends[s - 1], ends[s]); seq_stride is
+ * not used.  Ends beyond `tokens`, or that fall, are cut to what lies inside;
+ * outputs of tokens in no sequence are not written.
+ * log_decay: device, `heads` floats g, at most 0 in use: what a head's state
+ * keeps of itself from token to token is e^g (-inf: no memory).  The decays
+ * are constants of the model: there is no gradient for them.
+ */
+typedef struct {
+    int dtype;                        /* LIBSCAN_F32 / BF16 / F16, of all rows */
+    uint32_t seqs, heads, key_width, value_width;
+    uint64_t tokens;
+    const uint32_t *ends;
+    const float *log_decay;
+    float scale;
+} linattn_shape_t;
+
+/*
+ * The recurrence over the tokens t of each sequence and head,
+ *     S(t) = e^g S(t - 1) + k(t) v(t)^T,    out(t) = scale S(t)^T q(t),
+ * a prefix scan of (decay, key_width x value_width matrix) pairs, in its
+ * chunked form.  Sums are held in 32 bits; bf16 rows are multiplied as bf16,
+ * with the decayed scores and the state that a row reads rounded to bf16.
+ *
+ * state      device, [seqs][heads][key_width][value_width] floats: S before
+ *            the first token, or NULL for zeros.
+ * state_out  the same shape: S after the last token, or NULL.  An empty
+ *            sequence passes its state through.  May not be `state`.
+ * out        value_width wide, `heads` heads; overlaps no input.
+ * scratch    at least linattn_scratch_bytes(shape) bytes.
+ * Nothing at a token that is in no sequence is read; a value that is not
+ * finite reaches no earlier token and no other sequence.
+ * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type, widths, heads), ERR_SIZE
+ * (more than LIBSCAN_MAX_N tokens, or a grid too large), ERR_SCRATCH, ERR_HIP.
+ */
+size_t linattn_scratch_bytes(const linattn_shape_t *shape);
+int linattn(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
+            const linattn_rows_t *v, const float *state, const linattn_rows_t *out,
+            float *state_out, void *scratch, size_t scratch_bytes, hipStream_t stream);
+
+/*
+ * Its gradient.  dout is what out's gradient is, dstate_out (or NULL for
+ * zeros) state_out's; dq, dk and dv have as many heads as q, k and v (where
+ * heads share an input, their gradients are summed in 32 bits, in a fixed
+ * order), and dstate (or NULL) is the initial state's.  state is what the
+ * forward call had.  No output may overlap an input or another output.
+ */
+size_t linattn_grad_scratch_bytes(const linattn_shape_t *shape, uint32_t q_heads, uint32_t k_heads,
+                                  uint32_t v_heads);
+int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const linattn_rows_t *q,
+                 const linattn_rows_t *k, const linattn_rows_t *v, const float *state,
+                 const float *dstate_out, const linattn_rows_t *dq, const linattn_rows_t *dk,
+                 const linattn_rows_t *dv, float *dstate, void *scratch, size_t scratch_bytes,
+                 hipStream_t stream);
+
+/*
+ * One token of each of `seqs` rows (tokens and ends are not used; row r of a
+ * tensor starts at r * seq_stride).  Row r updates the state in slot slots[r]
+ * of a pool of `pool` states, or slot r when slots is NULL.  A row whose slot
+ * lies outside [0, pool) is idle: its output is zeros and it touches no
+ * state.  A slot may be listed once only.
+ *
+ * state      device, [pool][heads][key_width][value_width] floats.
+ * state_out  where the new states go: `state` itself, or a pool that does
+ *            not overlap it (slots of no row are left as they are).
+ */
+int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
+                 const linattn_rows_t *v, const float *state, uint64_t pool, const int32_t *slots,
+                 const linattn_rows_t *out, float *state_out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sampling a token from each row of logits                                 */
+/* ------------------------------------------------------------------------ */
+
+/* Largest vocabulary. */
+#define SAMPLE_MAX_VOCAB ((uint64_t)1 << 24)
+
+/*
+ * Per row, with x its logits, M the largest and w(i) = e^((x(i) - M) /
+ * temperature): of the tokens in order of falling x (equal ones by rising
+ * index; NaN and -inf are not in it) keep those with w >= min_p, at most the
+ * first top_k, and of these the fewest whose weight is at least top_p of
+ * theirs (one at least).  The token is the lowest kept index whose sum of
+ * kept weights, in index order up to and with it, is above u times their sum.
+ *
+ * temperature <= 0 or NaN  the lowest index of the largest logit
+ * top_k <= 0               no limit
+ * top_p >= 1 or NaN        off; <= 0 keeps one token
+ * min_p <= 0 or NaN        off; above 1 it counts as 1
+ * +inf logits              share all the weight
+ * u                        in [0, 1); what is outside is taken to the end it passed
+ * A row without a token gets token -1, logprob -inf and kept 0.
+ *
+ * Weights are 64-bit fixed point, 2^(62 - ceil log2 vocab) for the largest,
+ * rounded up, from 64-bit exponentials: their sums are the same in any order,
+ * and no token above weight zero is lost.
+ *
+ * logits       device, rows of `vocab` elements, row_stride elements apart.
+ * u            device, `rows` floats.
+ * temperatures, top_ks, top_ps, min_ps   device, one for each row, or NULL:
+ *              then temperature, top_k, top_p, min_p hold for all rows.
+ * tokens       device, `rows` int32.
+ * logprobs     device, `rows` floats, or NULL: log of the token's share of
+ *              the kept weights.
+ * kept         device, `rows` int32, or NULL: how many tokens were kept.
+ * scratch      at least sample_scratch_bytes(rows, vocab) bytes.
+ * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type), ERR_SIZE (vocab above
+ * SAMPLE_MAX_VOCAB, rows above 2^31 - 1), ERR_SCRATCH, ERR_HIP.
+ */
+typedef struct {
+    int dtype;                        /* LIBSCAN_F32 / BF16 / F16 */
+    uint64_t rows, vocab;
+    const void *logits;
+    int64_t row_stride;
+    const float *u;
+    float temperature, top_p, min_p;
+    int32_t top_k;
+    const float *temperatures, *top_ps, *min_ps;
+    const int32_t *top_ks;
+    int32_t *tokens;
+    float *logprobs;
+    int32_t *kept;
+} sample_args_t;
+
+size_t sample_scratch_bytes(uint64_t rows, uint64_t vocab);
+int sample_logits(const sample_args_t *args, void *scratch, size_t scratch_bytes,
+                  hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Measurement aid                                                          */

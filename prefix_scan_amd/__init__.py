@@ -9,6 +9,8 @@ a missing ``libscan.so`` raises.
 PyTorch supplies device memory and streams.  Tensors must be on a CUDA (HIP)
 device, contiguous, with 4-byte elements (torch.int32 or torch.uint32), or
 8-byte elements (torch.int64 or torch.uint64) for the *_u64 entry points.
+Rows of linear attention and of logits are float32, bfloat16 or float16, with
+any strides whose last is 1.
 """
 import ctypes
 import os
@@ -22,6 +24,7 @@ __all__ = [
     "scan_op_u32", "reduce_op_u32", "scan_op_u64", "reduce_op_u64",
     "runs_layout_u32", "runs_slots_i32", "runs_owner_u32", "runs_owner_all_u32",
     "segscan_flags_u32",
+    "linattn", "linattn_grad", "linattn_step", "sample_logits",
     "segscan_u32", "compact_flags_u32", "radix_perm_u32", "copy_u32", "scan_u32_noalloc",
     "scan_scratch_bytes", "scan_ex_scratch_bytes", "segscan_scratch_bytes",
     "compact_scratch_bytes", "radix_scratch_bytes",
@@ -42,6 +45,38 @@ class LibscanError(RuntimeError):
         self.status = status
         super().__init__("%s failed: %s (status %d)" % (what, lib().libscan_strerror(status).decode(),
                                                          status))
+
+
+LINATTN_MAX_WIDTH = 128
+SAMPLE_MAX_VOCAB = 1 << 24
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # LIBSCAN_F32 / BF16 / F16
+
+
+class _Rows(ctypes.Structure):
+    """linattn_rows_t"""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_uint32)]
+
+
+class _Shape(ctypes.Structure):
+    """linattn_shape_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("seqs", ctypes.c_uint32), ("heads", ctypes.c_uint32),
+                ("key_width", ctypes.c_uint32), ("value_width", ctypes.c_uint32),
+                ("tokens", ctypes.c_uint64), ("ends", ctypes.c_void_p),
+                ("log_decay", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class _Sample(ctypes.Structure):
+    """sample_args_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64),
+                ("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("u", ctypes.c_void_p), ("temperature", ctypes.c_float),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("temperatures", ctypes.c_void_p), ("top_ps", ctypes.c_void_p),
+                ("min_ps", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("tokens", ctypes.c_void_p), ("logprobs", ctypes.c_void_p),
+                ("kept", ctypes.c_void_p)]
 
 
 _lib = None
@@ -123,6 +158,22 @@ def lib():
         L.copy_u32.restype = i32
         L.scan_u32_noalloc.argtypes = [vp, u64, i32, vp, vp]
         L.scan_u32_noalloc.restype = i32
+        shape, rows = ctypes.POINTER(_Shape), ctypes.POINTER(_Rows)
+        L.linattn_scratch_bytes.argtypes = [shape]
+        L.linattn_scratch_bytes.restype = sz
+        L.linattn.argtypes = [shape, rows, rows, rows, vp, rows, vp, vp, sz, vp]
+        L.linattn.restype = i32
+        L.linattn_grad_scratch_bytes.argtypes = [shape] + [ctypes.c_uint32] * 3
+        L.linattn_grad_scratch_bytes.restype = sz
+        L.linattn_grad.argtypes = ([shape] + [rows] * 4 + [vp, vp] + [rows] * 3 +
+                                   [vp, vp, sz, vp])
+        L.linattn_grad.restype = i32
+        L.linattn_step.argtypes = [shape, rows, rows, rows, vp, u64, vp, rows, vp, vp]
+        L.linattn_step.restype = i32
+        L.sample_scratch_bytes.argtypes = [u64, u64]
+        L.sample_scratch_bytes.restype = sz
+        L.sample_logits.argtypes = [ctypes.POINTER(_Sample), vp, sz, vp]
+        L.sample_logits.restype = i32
         _lib = L
     return _lib
 
@@ -171,6 +222,7 @@ def _stream_handle(device, stream):
 # is initialised only when it is created.
 # --------------------------------------------------------------------------
 _scratch = {}
+_outgrown = []          # kept: a captured graph may hold their addresses
 _scratch_lock = threading.Lock()
 
 
@@ -185,6 +237,8 @@ def _scratch_for(device, stream_obj, nbytes):
             _check(lib().libscan_scratch_init(ctypes.c_void_p(buf.data_ptr()), size,
                                               ctypes.c_void_p(stream_obj.cuda_stream)),
                    "libscan_scratch_init")
+            if key in _scratch:
+                _outgrown.append(_scratch[key])
             _scratch[key] = buf
         return buf
 
@@ -527,3 +581,220 @@ def copy_u32(src, dst, stream=None):
     _check(lib().copy_u32(_ptr(src), _ptr(dst), src.numel(), _ptr(scr), scr.numel(), sh),
            "copy_u32")
     return dst
+
+
+# --------------------------------------------------------------------------
+# Linear attention with a decay for each head, and sampling
+# --------------------------------------------------------------------------
+
+def _dev_rows(t, name, dtype=None, dims=None, device=None):
+    """A tensor of float rows: any strides, its last dimension contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError("%s must be %s, got %s" % (
+            name, dtype or "float32, bfloat16 or float16", t.dtype))
+    if dims is not None and t.dim() != dims:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, dims, t.dim()))
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError("%s must be on %s, got %s" % (name, device or "a GPU device", t.device))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return t
+
+
+def _dev_dense(t, name, dtype, shape, device):
+    """A contiguous tensor of one type, shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _rows(t, packed):
+    """A [B, T, H, D] tensor's rows, a packed [N, H, D] one's or a step's [B, H, D]."""
+    seq, tok = (0, t.stride(0)) if packed else (t.stride(0), t.stride(1) if t.dim() == 4 else 0)
+    return _Rows(t.data_ptr(), seq, tok, t.stride(-2), t.shape[-2])
+
+
+def _shape_of(q, k, v, log_decay, scale, ends, dims):
+    _dev_rows(q, "q", dims=dims)
+    device = q.device
+    _dev_rows(k, "k", q.dtype, dims, device)
+    _dev_rows(v, "v", q.dtype, dims, device)
+    if k.shape[:-2] != q.shape[:-2] or v.shape[:-2] != q.shape[:-2]:
+        raise ValueError("q, k and v must have the same tokens, got %s, %s and %s" % (
+            tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    if k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must have the same width, got %d and %d" % (
+            q.shape[-1], k.shape[-1]))
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not 1 <= t.shape[-1] <= LINATTN_MAX_WIDTH:
+            raise ValueError("%s must be 1 to %d wide, got %d" % (
+                name, LINATTN_MAX_WIDTH, t.shape[-1]))
+    if not isinstance(log_decay, torch.Tensor) or log_decay.dim() != 1:
+        raise TypeError("log_decay must be a torch.Tensor of one float for each head")
+    heads = log_decay.shape[0]
+    _dev_dense(log_decay, "log_decay", torch.float32, (heads,), device)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.shape[-2] == 0 or heads % t.shape[-2]:
+            raise ValueError("the heads of %s (%d) must divide log_decay's %d" % (
+                name, t.shape[-2], heads))
+    seqs = q.shape[0]
+    if ends is not None:
+        _dev_u32(ends, "ends")
+        if ends.device != device or ends.dim() != 1:
+            raise ValueError("ends must be one number for each sequence, on %s" % device)
+        seqs = ends.shape[0]
+    return _Shape(_DTYPES[q.dtype], seqs, heads, q.shape[-1], v.shape[-1],
+                  q.shape[-3] if dims == 4 or ends is not None else 1,
+                  ends.data_ptr() if ends is not None else None, log_decay.data_ptr(), float(scale))
+
+
+def _states(shape, t, name, device, count=None):
+    return None if t is None else _dev_dense(
+        t, name, torch.float32,
+        (shape.seqs if count is None else count, shape.heads, shape.key_width, shape.value_width),
+        device)
+
+
+def _new_states(shape, device):
+    return torch.empty((shape.seqs, shape.heads, shape.key_width, shape.value_width),
+                       dtype=torch.float32, device=device)
+
+
+def _out_like(out, name, want, dtype, device):
+    """`out`, checked, or a new tensor of that shape."""
+    if out is None:
+        return torch.empty(want, dtype=dtype, device=device)
+    _dev_rows(out, name, dtype, len(want), device)
+    if tuple(out.shape) != tuple(want):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(want), tuple(out.shape)))
+    return out
+
+
+def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=False, out=None,
+            state_out=None, stream=None):
+    """Linear attention with a decay for each head, over whole sequences:
+    S(t) = exp(log_decay) S(t-1) + k(t) v(t)^T, out(t) = scale S(t)^T q(t).
+
+    q, k [B, T, H, Dk] and v [B, T, H, Dv] (k, v and q may have fewer heads,
+    each shared by consecutive ones); with ends (int32 [B], as
+    runs_layout_u32 leaves them) [N, H, D], the sequences one after another.
+    state: float32 [B, H, Dk, Dv] before the first token (None: zeros).
+    Returns (out, state_out), state_out None unless want_state or given."""
+    packed = ends is not None
+    shape = _shape_of(q, k, v, log_decay, scale, ends, 3 if packed else 4)
+    _states(shape, state, "state", q.device)
+    out = _out_like(out, "out", q.shape[:-2] + (shape.heads, shape.value_width), q.dtype, q.device)
+    if state_out is None and want_state:
+        state_out = _new_states(shape, q.device)
+    _states(shape, state_out, "state_out", q.device)
+    sh, s = _stream_handle(q.device, stream)
+    scr = _scratch_for(q.device, s, lib().linattn_scratch_bytes(shape))
+    _check(lib().linattn(shape, _rows(q, packed), _rows(k, packed), _rows(v, packed), _ptr(state),
+                         _rows(out, packed), _ptr(state_out), _ptr(scr), scr.numel(), sh),
+           "linattn")
+    return out, state_out
+
+
+def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dstate_out=None,
+                 want_dstate=False, dq=None, dk=None, dv=None, dstate=None, stream=None):
+    """The gradient of linattn: (dq, dk, dv, dstate) for out's gradient dout
+    and state_out's dstate_out (None: zeros); dstate is None unless
+    want_dstate or given.  Gradients of shared heads are summed."""
+    packed = ends is not None
+    shape = _shape_of(q, k, v, log_decay, scale, ends, 3 if packed else 4)
+    _dev_rows(dout, "dout", q.dtype, q.dim(), q.device)
+    if tuple(dout.shape) != tuple(q.shape[:-2]) + (shape.heads, shape.value_width):
+        raise ValueError("dout must have the shape of linattn's out, got %s" % (tuple(dout.shape),))
+    _states(shape, state, "state", q.device)
+    _states(shape, dstate_out, "dstate_out", q.device)
+    dq = _out_like(dq, "dq", q.shape, q.dtype, q.device)
+    dk = _out_like(dk, "dk", k.shape, q.dtype, q.device)
+    dv = _out_like(dv, "dv", v.shape, q.dtype, q.device)
+    if dstate is None and want_dstate:
+        dstate = _new_states(shape, q.device)
+    _states(shape, dstate, "dstate", q.device)
+    sh, s = _stream_handle(q.device, stream)
+    scr = _scratch_for(q.device, s, lib().linattn_grad_scratch_bytes(
+        shape, q.shape[-2], k.shape[-2], v.shape[-2]))
+    _check(lib().linattn_grad(shape, _rows(dout, packed), _rows(q, packed), _rows(k, packed),
+                              _rows(v, packed), _ptr(state), _ptr(dstate_out), _rows(dq, packed),
+                              _rows(dk, packed), _rows(dv, packed), _ptr(dstate), _ptr(scr),
+                              scr.numel(), sh), "linattn_grad")
+    return dq, dk, dv, dstate
+
+
+def linattn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, state_out=None,
+                 stream=None):
+    """One token of each row of linattn's recurrence: q, k [B, H, Dk] and
+    v [B, H, Dv]; row r updates state[slots[r]] (state[r] without slots) of
+    the float32 pool [P, H, Dk, Dv], in place or into state_out.  A row whose
+    slot is outside the pool, as -1, gives zeros and touches nothing; no slot
+    may be listed twice.  Returns (out, the pool that was written)."""
+    shape = _shape_of(q, k, v, log_decay, scale, None, 3)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise TypeError("state must be a torch.Tensor of [P, H, Dk, Dv]")
+    pool = state.shape[0]
+    _states(shape, state, "state", q.device, pool)
+    state_out = state if state_out is None else _states(shape, state_out, "state_out", q.device, pool)
+    if slots is None:
+        if pool != shape.seqs:
+            raise ValueError("without slots, state must hold one state for each of %d rows, got %d"
+                             % (shape.seqs, pool))
+    else:
+        _dev_dense(slots, "slots", torch.int32, (shape.seqs,), q.device)
+    out = _out_like(out, "out", (shape.seqs, shape.heads, shape.value_width), q.dtype, q.device)
+    sh, _ = _stream_handle(q.device, stream)
+    _check(lib().linattn_step(shape, _rows(q, False), _rows(k, False), _rows(v, False), _ptr(state),
+                              pool, _ptr(slots), _rows(out, False), _ptr(state_out), sh),
+           "linattn_step")
+    return out, state_out
+
+
+def sample_logits(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None,
+                  logprobs=None, kept=None, stream=None):
+    """One token from each row of logits [R, V] by the random numbers u
+    (float32 [R], in [0, 1)); temperature, top_k, top_p and min_p are numbers
+    or tensors with one for each row (float32, and int32 for top_k).
+
+    Of the tokens by falling logit, those with at least min_p of the largest
+    one's weight are kept, top_k of them at most, then the fewest whose
+    weight is at least top_p; the token is where u of the kept weights, in
+    index order, is passed.  temperature 0 is the largest logit.  Returns
+    (tokens int32, logprobs float32, kept int32); a row with nothing but -inf
+    and NaN gets token -1."""
+    _dev_rows(logits, "logits", dims=2)
+    device, rows = logits.device, logits.shape[0]
+    if logits.shape[1] > SAMPLE_MAX_VOCAB:
+        raise ValueError("logits must have at most %d columns, got %d" % (
+            SAMPLE_MAX_VOCAB, logits.shape[1]))
+    _dev_dense(u, "u", torch.float32, (rows,), device)
+    a = _Sample(_DTYPES[logits.dtype], rows, logits.shape[1], logits.data_ptr(), logits.stride(0),
+                u.data_ptr())
+    for value, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
+                               (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        if isinstance(value, torch.Tensor):
+            _dev_dense(value, name, dtype, (rows,), device)
+            setattr(a, name + "s", value.data_ptr())
+        else:
+            setattr(a, name, min(max(int(value), 0), 0x7FFFFFFF) if name == "top_k" else float(value))
+    outs = []
+    for t, name, dtype in ((tokens, "tokens", torch.int32), (logprobs, "logprobs", torch.float32),
+                           (kept, "kept", torch.int32)):
+        t = torch.empty(rows, dtype=dtype, device=device) if t is None else \
+            _dev_dense(t, name, dtype, (rows,), device)
+        setattr(a, name, t.data_ptr())
+        outs.append(t)
+    sh, s = _stream_handle(device, stream)
+    scr = _scratch_for(device, s, lib().sample_scratch_bytes(rows, logits.shape[1]))
+    _check(lib().sample_logits(a, _ptr(scr), scr.numel(), sh), "sample_logits")
+    return tuple(outs)

@@ -3,6 +3,8 @@
 // total or count.  All GPU work is enqueued on the caller's stream.
 #include "../../include/libscan.h"
 #include "launch.hpp"
+#include "linattn.hpp"
+#include "sample.hpp"
 #include "scratch_state.hpp"
 
 #include <stdio.h>
@@ -250,6 +252,106 @@ struct NoallocDevice {
 std::mutex g_noalloc_mu;
 NoallocDevice g_noalloc[kNoallocMaxDevices];
 
+
+// ---------------------------------------------------------------------------
+// Linear attention: checks and the sweeps of a call (linattn.hpp).
+// ---------------------------------------------------------------------------
+
+size_t element_bytes(int dtype) { return dtype == LIBSCAN_F32 ? 4 : 2; }
+
+bool bad_type(int dtype) { return dtype < LIBSCAN_F32 || dtype > LIBSCAN_F16; }
+
+int check_shape(const linattn_shape_t *s)
+{
+    if (!s)
+        return LIBSCAN_ERR_NULL;
+    if (bad_type(s->dtype) || s->heads == 0 || s->key_width == 0 || s->value_width == 0 ||
+        s->key_width > LINATTN_MAX_WIDTH || s->value_width > LINATTN_MAX_WIDTH)
+        return LIBSCAN_ERR_ARG;
+    if (s->heads > 65535 || s->seqs > (1u << 24) || s->tokens > LIBSCAN_MAX_N)
+        return LIBSCAN_ERR_SIZE;
+    if (misaligned4(s->ends) || misaligned4(s->log_decay))
+        return LIBSCAN_ERR_ALIGN;
+    return LIBSCAN_OK;
+}
+
+// `any`: the rows hold something (else the tensor's pointer is not looked at).
+int check_rows(const linattn_shape_t &s, const linattn_rows_t *r, bool any, bool output)
+{
+    if (!r)
+        return LIBSCAN_ERR_NULL;
+    if (r->heads == 0 || s.heads % r->heads != 0 || (output && r->heads != s.heads))
+        return LIBSCAN_ERR_ARG;
+    if ((uintptr_t)r->data % element_bytes(s.dtype) != 0)
+        return LIBSCAN_ERR_ALIGN;
+    if (any && !r->data)
+        return LIBSCAN_ERR_NULL;
+    return LIBSCAN_OK;
+}
+
+Rows rows_of(const linattn_shape_t &s, const linattn_rows_t &r)
+{
+    return Rows{r.data, s.ends ? 0 : r.seq_stride, r.token_stride, r.head_stride, s.heads / r.heads};
+}
+
+bool rows_aligned(const linattn_shape_t &s, const Rows &r, uint32_t width)
+{
+    const size_t b = element_bytes(s.dtype);
+    return (uintptr_t)r.p % 16 == 0 && width * b % 16 == 0 && r.seq * (int64_t)b % 16 == 0 &&
+           r.tok * (int64_t)b % 16 == 0 && r.head * (int64_t)b % 16 == 0;
+}
+
+// Everything of a set but its sweeps.
+SweepSet sweep_set(const linattn_shape_t &s, int count)
+{
+    SweepSet set = {};
+    set.count = count;
+    set.dtype = s.dtype;
+    set.log_decay = s.log_decay;
+    set.ends = s.ends;
+    set.seqs = s.seqs;
+    set.heads = s.heads;
+    set.tokens = s.tokens;
+    set.seg_len = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count);
+    set.items = (uint32_t)linattn_items(s.tokens, s.ends != nullptr, s.seqs, set.seg_len);
+    return set;
+}
+
+size_t segment_bytes(const linattn_shape_t &s, int count)
+{
+    const SweepSet set = sweep_set(s, count);
+    if (!set.seg_len)
+        return 0;
+    const int width = (int)(s.key_width > s.value_width ? s.key_width : s.value_width);
+    return round_up((size_t)count * set.items * s.heads * linattn_state_floats(width) * sizeof(float),
+                    kScratchAlign);
+}
+
+bool too_many_items(const linattn_shape_t &s, int count)
+{
+    const uint64_t l = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count);
+    return linattn_items(s.tokens, s.ends != nullptr, s.seqs, l) > (1u << 26);
+}
+
+uint64_t all_rows(const linattn_shape_t &s) { return s.ends ? s.tokens : s.tokens * s.seqs; }
+
+// Float rows of every head, for the gradients of a tensor with shared heads.
+size_t partial_bytes(const linattn_shape_t &s, uint32_t heads, uint32_t width)
+{
+    if (heads == s.heads)
+        return 0;
+    return round_up((size_t)all_rows(s) * s.heads * width * sizeof(float), kScratchAlign);
+}
+
+void out_of(const linattn_shape_t &s, Sweep &w, const linattn_rows_t &r, float *partial, uint32_t width)
+{
+    w.out_f32 = r.heads != s.heads;
+    w.out = w.out_f32 ? partial : r.data;
+    w.out_head = w.out_f32 ? (int64_t)width : r.head_stride;
+    w.out_tok = w.out_f32 ? (int64_t)s.heads * width : r.token_stride;
+    w.out_seq = s.ends ? 0 : (w.out_f32 ? (int64_t)s.tokens * s.heads * width : r.seq_stride);
+}
+
 }  // namespace
 
 static __device__ __align__(256) uint8_t noalloc_scratch[kNoallocBytes];
@@ -311,7 +413,7 @@ const char *libscan_strerror(int status)
     case LIBSCAN_ERR_ARG: return "an argument is outside its documented range";
     case LIBSCAN_ERR_SCRATCH: return "scratch buffer is smaller than the size query's answer";
     case LIBSCAN_ERR_HIP: return hipGetErrorString(g_last_hip);
-    case LIBSCAN_ERR_ALIGN: return "a pointer is not 4-byte aligned";
+    case LIBSCAN_ERR_ALIGN: return "a pointer is not aligned to its elements";
     default: return "unknown libscan status";
     }
 }
@@ -775,6 +877,237 @@ int copy_u32(const uint32_t *src, uint32_t *dst, uint64_t n, void *scratch, size
     hipError_t e = prepare_state(s, kKindDesc, 0, 0, 1, stream);
     if (e == hipSuccess)
         e = launch_copy(src, dst, n, s, stream);
+    return hip_status(e);
+}
+
+size_t linattn_scratch_bytes(const linattn_shape_t *shape)
+{
+    if (check_shape(shape) != LIBSCAN_OK || shape->seqs == 0 || too_many_items(*shape, 1))
+        return with_header(0);
+    return with_header(segment_bytes(*shape, 1));
+}
+
+int linattn(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
+            const linattn_rows_t *v, const float *state, const linattn_rows_t *out,
+            float *state_out, void *scratch, size_t scratch_bytes, hipStream_t stream)
+{
+    int rc = check_shape(shape);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    const linattn_shape_t &sh = *shape;
+    const bool any = sh.seqs != 0 && sh.tokens != 0;
+    if ((rc = check_rows(sh, q, any, false)) != LIBSCAN_OK ||
+        (rc = check_rows(sh, k, any, false)) != LIBSCAN_OK ||
+        (rc = check_rows(sh, v, any, false)) != LIBSCAN_OK ||
+        (rc = check_rows(sh, out, any, true)) != LIBSCAN_OK)
+        return rc;
+    if (misaligned4(state) || misaligned4(state_out))
+        return LIBSCAN_ERR_ALIGN;
+    if (sh.seqs == 0)
+        return LIBSCAN_OK;
+    if (!sh.log_decay || !scratch)
+        return LIBSCAN_ERR_NULL;
+    if (state && state == state_out)
+        return LIBSCAN_ERR_ARG;
+    if (too_many_items(sh, 1))
+        return LIBSCAN_ERR_SIZE;
+    Scratch s;
+    if (!carve(scratch, scratch_bytes, segment_bytes(sh, 1), &s))
+        return LIBSCAN_ERR_SCRATCH;
+    SweepSet set = sweep_set(sh, 1);
+    set.seg = reinterpret_cast<float *>(s.body());
+    Sweep &w = set.s[0];
+    w.a = rows_of(sh, *q);
+    w.b = rows_of(sh, *k);
+    w.c = rows_of(sh, *v);
+    out_of(sh, w, *out, nullptr, sh.value_width);
+    w.m = (int)sh.key_width;
+    w.n = (int)sh.value_width;
+    w.pair_scale = 1.f;
+    w.out_scale = sh.scale;
+    // The state enters each row's sum before out_scale.
+    w.state_in = state;
+    w.state_out = state_out;
+    w.state_m = sh.value_width;
+    w.state_n = 1;
+    set.aligned = rows_aligned(sh, w.a, sh.key_width) && rows_aligned(sh, w.b, sh.key_width) &&
+                  rows_aligned(sh, w.c, sh.value_width);
+    hipError_t e = prepare_state(s, kKindData, 0, 0, 0, stream);
+    if (e == hipSuccess)
+        e = launch_sweeps(set, stream);
+    return hip_status(e);
+}
+
+size_t linattn_grad_scratch_bytes(const linattn_shape_t *shape, uint32_t q_heads, uint32_t k_heads,
+                                  uint32_t v_heads)
+{
+    if (check_shape(shape) != LIBSCAN_OK || shape->seqs == 0 || too_many_items(*shape, 3))
+        return with_header(0);
+    return with_header(segment_bytes(*shape, 3) + partial_bytes(*shape, q_heads, shape->key_width) +
+                       partial_bytes(*shape, k_heads, shape->key_width) +
+                       partial_bytes(*shape, v_heads, shape->value_width));
+}
+
+int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const linattn_rows_t *q,
+                 const linattn_rows_t *k, const linattn_rows_t *v, const float *state,
+                 const float *dstate_out, const linattn_rows_t *dq, const linattn_rows_t *dk,
+                 const linattn_rows_t *dv, float *dstate, void *scratch, size_t scratch_bytes,
+                 hipStream_t stream)
+{
+    int rc = check_shape(shape);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    const linattn_shape_t &sh = *shape;
+    const bool any = sh.seqs != 0 && sh.tokens != 0;
+    if ((rc = check_rows(sh, dout, any, true)) != LIBSCAN_OK)
+        return rc;
+    const linattn_rows_t *in[3] = {q, k, v}, *grad[3] = {dq, dk, dv};
+    for (int i = 0; i < 3; ++i) {
+        if ((rc = check_rows(sh, in[i], any, false)) != LIBSCAN_OK ||
+            (rc = check_rows(sh, grad[i], any, false)) != LIBSCAN_OK)
+            return rc;
+        if (in[i]->heads != grad[i]->heads)
+            return LIBSCAN_ERR_ARG;
+    }
+    if (misaligned4(state) || misaligned4(dstate_out) || misaligned4(dstate))
+        return LIBSCAN_ERR_ALIGN;
+    if (sh.seqs == 0)
+        return LIBSCAN_OK;
+    if (!sh.log_decay || !scratch)
+        return LIBSCAN_ERR_NULL;
+    if (dstate && (dstate == state || dstate == dstate_out))
+        return LIBSCAN_ERR_ARG;
+    if (too_many_items(sh, 3))
+        return LIBSCAN_ERR_SIZE;
+    const uint32_t kw = sh.key_width, vw = sh.value_width, width[3] = {kw, kw, vw};
+    size_t at = segment_bytes(sh, 3), partial[3];
+    for (int i = 0; i < 3; ++i) {
+        partial[i] = at;
+        at += partial_bytes(sh, in[i]->heads, width[i]);
+    }
+    Scratch s;
+    if (!carve(scratch, scratch_bytes, at, &s))
+        return LIBSCAN_ERR_SCRATCH;
+    SweepSet set = sweep_set(sh, 3);
+    set.seg = reinterpret_cast<float *>(s.body());
+    const Rows rq = rows_of(sh, *q), rk = rows_of(sh, *k), rv = rows_of(sh, *v),
+               ro = rows_of(sh, *dout);
+    const Rows abc[3][3] = {{ro, rv, rk}, {rv, ro, rq}, {rk, rq, ro}};
+    for (int i = 0; i < 3; ++i) {
+        Sweep &w = set.s[i];
+        w.a = abc[i][0];
+        w.b = abc[i][1];
+        w.c = abc[i][2];
+        out_of(sh, w, *grad[i], reinterpret_cast<float *>(s.body() + partial[i]), width[i]);
+        w.m = (int)(i == 2 ? kw : vw);
+        w.n = (int)(i == 2 ? vw : kw);
+        w.rev = w.shift = i != 0;
+        // dq is scaled as a whole; the gradient of the final state reaches
+        // dk and dv unscaled, so there the pairs are.
+        w.pair_scale = i == 0 ? 1.f : sh.scale;
+        w.out_scale = i == 0 ? sh.scale : 1.f;
+        w.state_in = i == 0 ? state : dstate_out;
+        w.state_out = i == 2 ? dstate : nullptr;
+        w.state_m = i == 2 ? (int64_t)vw : 1;
+        w.state_n = i == 2 ? 1 : (int64_t)vw;
+    }
+    set.aligned = rows_aligned(sh, rq, kw) && rows_aligned(sh, rk, kw) && rows_aligned(sh, rv, vw) &&
+                  rows_aligned(sh, ro, vw);
+    hipError_t e = prepare_state(s, kKindData, 0, 0, 0, stream);
+    if (e == hipSuccess)
+        e = launch_sweeps(set, stream);
+    for (int i = 0; i < 3 && e == hipSuccess; ++i) {
+        if (!set.s[i].out_f32)
+            continue;
+        HeadSum h = {};
+        h.src = static_cast<const float *>(set.s[i].out);
+        h.dst = rows_of(sh, *grad[i]);
+        h.seqs = sh.ends ? 1 : sh.seqs;
+        h.tokens = sh.tokens;
+        h.heads = grad[i]->heads;
+        h.share = sh.heads / grad[i]->heads;
+        h.width = (int)width[i];
+        h.dtype = sh.dtype;
+        e = launch_head_sum(h, stream);
+    }
+    return hip_status(e);
+}
+
+int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
+                 const linattn_rows_t *v, const float *state, uint64_t pool, const int32_t *slots,
+                 const linattn_rows_t *out, float *state_out, hipStream_t stream)
+{
+    int rc = check_shape(shape);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    const linattn_shape_t &sh = *shape;
+    const bool any = sh.seqs != 0;
+    if ((rc = check_rows(sh, q, any, false)) != LIBSCAN_OK ||
+        (rc = check_rows(sh, k, any, false)) != LIBSCAN_OK ||
+        (rc = check_rows(sh, v, any, false)) != LIBSCAN_OK ||
+        (rc = check_rows(sh, out, any, true)) != LIBSCAN_OK)
+        return rc;
+    if (misaligned4(state) || misaligned4(state_out) || misaligned4(slots))
+        return LIBSCAN_ERR_ALIGN;
+    if (!any)
+        return LIBSCAN_OK;
+    if (!sh.log_decay || ((!state || !state_out) && pool != 0))
+        return LIBSCAN_ERR_NULL;
+    if (pool > LIBSCAN_MAX_N)
+        return LIBSCAN_ERR_SIZE;
+    StepArgs a = {};
+    // Rows are the sequences here, packed or not.
+    const linattn_rows_t *rows[4] = {q, k, v, out};
+    Rows *to[4] = {&a.q, &a.k, &a.v, &a.out};
+    for (int i = 0; i < 4; ++i)
+        *to[i] = Rows{rows[i]->data, rows[i]->seq_stride, 0, rows[i]->head_stride,
+                      sh.heads / rows[i]->heads};
+    a.dtype = sh.dtype;
+    a.dk = (int)sh.key_width;
+    a.dv = (int)sh.value_width;
+    a.rows = sh.seqs;
+    a.heads = sh.heads;
+    a.log_decay = sh.log_decay;
+    a.scale = sh.scale;
+    a.state = state;
+    a.state_out = state_out;
+    a.pool = pool;
+    a.slots = slots;
+    return hip_status(launch_linattn_step(a, stream));
+}
+
+size_t sample_scratch_bytes(uint64_t rows, uint64_t vocab)
+{
+    if (rows > LIBSCAN_MAX_N_INDEX || vocab > SAMPLE_MAX_VOCAB)
+        return with_header(0);
+    return with_header(sample_body_bytes(rows, vocab));
+}
+
+int sample_logits(const sample_args_t *args, void *scratch, size_t scratch_bytes,
+                  hipStream_t stream)
+{
+    if (!args)
+        return LIBSCAN_ERR_NULL;
+    const sample_args_t &a = *args;
+    if (bad_type(a.dtype))
+        return LIBSCAN_ERR_ARG;
+    if (a.vocab > SAMPLE_MAX_VOCAB || a.rows > LIBSCAN_MAX_N_INDEX)
+        return LIBSCAN_ERR_SIZE;
+    if ((uintptr_t)a.logits % element_bytes(a.dtype) != 0 || misaligned4(a.u) ||
+        misaligned4(a.temperatures) || misaligned4(a.top_ps) || misaligned4(a.min_ps) ||
+        misaligned4(a.top_ks) || misaligned4(a.tokens) || misaligned4(a.logprobs) ||
+        misaligned4(a.kept))
+        return LIBSCAN_ERR_ALIGN;
+    if (a.rows == 0)
+        return LIBSCAN_OK;
+    if ((!a.logits && a.vocab != 0) || !a.u || !a.tokens || !scratch)
+        return LIBSCAN_ERR_NULL;
+    Scratch s;
+    if (!carve(scratch, scratch_bytes, sample_body_bytes(a.rows, a.vocab), &s))
+        return LIBSCAN_ERR_SCRATCH;
+    hipError_t e = prepare_state(s, kKindData, 0, 0, 0, stream);
+    if (e == hipSuccess)
+        e = launch_sample(a, s.body(), stream);
     return hip_status(e);
 }
 

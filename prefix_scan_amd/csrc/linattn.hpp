@@ -1,0 +1,215 @@
+// linattn.hpp -- what the linear-attention kernels and their host code share.
+//
+// Linear attention with a decay is a prefix scan whose elements are pairs
+// (decay, matrix) under (l, S) o (r, U) = (l r, r S + U).  Every product the
+// operator and its gradient need is one "sweep" over the tokens of a
+// sequence, in their order or in reverse:
+//
+//   out(i) = out_scale * ( sum_{j <= i} p^(i-j) pair_scale (a_i . b_j) c_j
+//                          + p^(i+1-shift) Z0^T a_i )            p = e^g
+//   Zend   = p^len Z0 + sum_j p^(len-1+shift-j) pair_scale b_j c_j^T
+//
+// with a, b of width m, c and out of width n and Z an m x n state:
+//   forward    a, b, c = q, k, v     order forward,  shift 0
+//   dq         a, b, c = do, v, k    order forward,  shift 0, Z transposed
+//   dk         a, b, c = v, do, q    order reversed, shift 1, Z transposed
+//   dv         a, b, c = k, q, do    order reversed, shift 1
+// (dk(t) = R(t) v(t), dv(t) = R(t)^T k(t) with R the decayed sum of
+// scale q do^T over the later tokens, to which the gradient of the final
+// state enters undecayed at the last token: shift 1.)
+//
+// A sequence is cut into segments of seg_len tokens, one workgroup each, so
+// that few long sequences still fill the GPU: a first kernel sums every
+// segment's own contribution to the state, a second scans those sums along
+// the sequence, and the third sweeps each segment from its entering state.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace libscan {
+
+constexpr int kMaxSweeps = 3;
+constexpr int kLinattnWidth = 128;      // largest m and n
+
+// Rows of one tensor: token t of sequence s, head h starts at element
+// s * seq + t * tok + (h / share) * head.
+struct Rows {
+    const void *p;
+    int64_t seq, tok, head;
+    uint32_t share;
+};
+
+struct Sweep {
+    Rows a, b, c;
+    void *out;
+    int64_t out_seq, out_tok, out_head;
+    int m, n;
+    int rev, shift;
+    int out_f32;                 // out holds floats (partial gradients of shared heads)
+    float pair_scale, out_scale;
+    const float *state_in;       // per (sequence, head) m * n floats, or null
+    float *state_out;
+    int64_t state_m, state_n;    // element strides of a state's two axes
+};
+
+struct SweepSet {
+    Sweep s[kMaxSweeps];
+    int count;
+    int dtype;                   // LIBSCAN_F32 / BF16 / F16
+    const float *log_decay;      // [heads]
+    const uint32_t *ends;        // inclusive run ends, or null: `tokens` per sequence
+    uint32_t seqs, heads;
+    uint64_t tokens;             // of each sequence, or in all when ends is given
+    uint64_t seg_len;            // 0: sequences are not cut
+    uint32_t items;              // workgroups along the tokens
+    float *seg;                  // segment states (when seg_len != 0)
+    bool aligned;                // every row starts on 16 bytes and is a whole number of them
+};
+
+// Tokens per segment for a set of sweeps (0: no cutting) and the number of
+// (sequence, segment) items a grid has to cover.
+uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps);
+uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len);
+// Floats of segment states one item of one head of one sweep takes.
+size_t linattn_state_floats(int width);
+
+hipError_t launch_sweeps(const SweepSet &set, hipStream_t stream);
+
+// Sums the `share` consecutive heads of float rows into rows of `dtype`.
+struct HeadSum {
+    const float *src;            // [seqs][tokens][heads * share][width], dense
+    Rows dst;                    // share unused
+    uint64_t tokens, seqs;
+    uint32_t heads, share;
+    int width, dtype;
+};
+hipError_t launch_head_sum(const HeadSum &h, hipStream_t stream);
+
+struct StepArgs {
+    Rows q, k, v, out;           // seq is the stride of a row
+    int dtype, dk, dv;
+    uint32_t rows, heads;
+    const float *log_decay;
+    float scale;
+    const float *state;
+    float *state_out;
+    uint64_t pool;
+    const int32_t *slots;
+};
+hipError_t launch_linattn_step(const StepArgs &a, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// e^(g n) for n >= 0, with e^(g 0) = 1 for every g (a head without memory
+// has g = -inf), as the nearest float and what that leaves.  A state is
+// decayed once a chunk by the same power: with the rounded one alone its
+// error would grow with every chunk (2^-25 of the state each time, and always
+// to one side), so states are multiplied by both parts.
+struct Power {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Power decay_power(float g, double n)
+{
+    const double x = n == 0.0 ? 1.0 : exp((double)g * n);
+    const float hi = (float)x;
+    const float lo = (float)(x - (double)hi);
+    return Power{hi, lo == lo ? lo : 0.f};      // hi may be infinite
+}
+
+__device__ __forceinline__ float decayed(float x, Power p)
+{
+    return __builtin_fmaf(x, p.hi, x * p.lo);
+}
+
+// Which sequence, and which segment of it, a workgroup has.
+struct Place {
+    uint32_t seq;
+    uint64_t first;      // token of the packed batch the sequence starts at (0 when dense)
+    uint64_t len;        // tokens of the sequence
+    uint64_t lo, hi;     // the segment, in the sweep's order
+    bool last;
+};
+
+__device__ __forceinline__ uint32_t wave_incl_u32(uint32_t x)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(x, d);
+        if ((int)(threadIdx.x & 63) >= d)
+            x += y;
+    }
+    return x;
+}
+
+// Sequence i of a packed batch.  Ends past the batch, or falling ones, are
+// cut to it, so that no list of ends reaches outside the rows.
+__device__ __forceinline__ void run_of(const uint32_t *ends, uint64_t tokens, uint32_t i,
+                                       uint64_t *first, uint64_t *len)
+{
+    const uint64_t lo = i ? ends[i - 1] : 0u, hi = ends[i];
+    const uint64_t a = lo < tokens ? lo : tokens, b = hi < tokens ? hi : tokens;
+    *first = a;
+    *len = b > a ? b - a : 0;
+}
+
+// Every sequence has max(1, ceil(len / seg_len)) items, in order.  False: the
+// item is past the last one.  One wave reads 64 run ends at a time.
+__device__ __forceinline__ bool place_of(const SweepSet &set, uint32_t item, Place *p)
+{
+    const uint64_t L = set.seg_len;
+    uint64_t s;
+    if (!set.ends) {
+        const uint64_t n = L && set.tokens ? (set.tokens + L - 1) / L : 1;
+        p->seq = (uint32_t)(item / n);
+        s = item % n;
+        p->first = 0;
+        p->len = set.tokens;
+        if (p->seq >= set.seqs)
+            return false;
+    } else if (!L) {
+        if (item >= set.seqs)
+            return false;
+        p->seq = item;
+        s = 0;
+        run_of(set.ends, set.tokens, item, &p->first, &p->len);
+    } else {
+        uint32_t before = 0;
+        bool found = false;
+        s = 0;
+        for (uint32_t i0 = 0; i0 < set.seqs && !found; i0 += 64) {
+            const uint32_t i = i0 + (threadIdx.x & 63);
+            uint64_t first = 0, len = 0;
+            uint32_t n = 0;
+            if (i < set.seqs) {
+                run_of(set.ends, set.tokens, i, &first, &len);
+                n = len ? (uint32_t)((len + L - 1) / L) : 1u;
+            }
+            const uint32_t incl = wave_incl_u32(n);
+            const uint64_t hit = __ballot(before + incl > item);
+            if (hit) {
+                const int src = __ffsll((unsigned long long)hit) - 1;
+                p->seq = i0 + src;
+                s = item - (before + __shfl(incl - n, src));
+                found = true;
+            }
+            before += __shfl(incl, 63);
+        }
+        if (!found)
+            return false;
+        run_of(set.ends, set.tokens, p->seq, &p->first, &p->len);
+    }
+    p->lo = L ? s * L : 0;
+    p->hi = L && p->lo + L < p->len ? p->lo + L : p->len;
+    p->last = p->hi == p->len;
+    return true;
+}
+
+}  // namespace libscan
