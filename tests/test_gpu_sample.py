@@ -155,3 +155,51 @@ def test_captured_and_replayed_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), rep
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_cuts_among_thousands_of_equal_logits(dtype):
+    # More tokens in the cut's bin, or under top_k, than a list holds.
+    x = torch.zeros((4, 20011), dtype=DTYPES[dtype])
+    x[1, ::2] = 1.0
+    x[2] = (torch.arange(20011) % 7).to(DTYPES[dtype]) / 1024        # inside the first bin
+    x[3] = logits(1, 20011, dtype, 11)[0]
+    for s in ({"top_k": 9999}, {"top_p": 0.5}, {"top_k": 15000, "top_p": 0.75}, {"top_k": 20010},
+              {"top_k": 12000, "top_p": 0.25, "min_p": 0.3}, {"top_p": 0.9999, "temperature": 50.0}):
+        for u in (0.0, 0.61, 0.99999994):
+            check(x, np.full(4, u), **s)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_scales_of_logits(dtype):
+    # All logits within one step of another, and spread over the type's range.
+    gen = torch.Generator().manual_seed(12)
+    base = torch.randn((5, 9001), generator=gen)
+    x = torch.stack([base[0] * 1e-4, base[1] * 0.01 + 100.0, base[2] * 5000.0, base[3] * 1e-30,
+                     base[4].exp() * 3]).to(DTYPES[dtype])
+    for s in ({}, {"top_p": 0.9}, {"top_k": 50, "top_p": 0.8}, {"temperature": 1e-3, "top_p": 0.9},
+              {"temperature": 3e38, "top_p": 0.5}, {"temperature": 1e-38, "top_p": 0.9}):
+        check(x, uniform(5, 13), **s)
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+def test_rows_that_start_anywhere(rows):
+    for dtype in DTYPES:
+        for vocab in (37, 1021):
+            x = logits(rows, vocab, dtype, 14)
+            u = torch.from_numpy(uniform(rows)).cuda()
+            want = ps.sample_logits(x.cuda(), u, 0.9, 30, 0.95)
+            for stride, at in ((vocab + 1, 1), (vocab + 3, 2), (2 * vocab + 5, 5)):
+                flat = torch.full((rows * stride + 8,), 60.0, dtype=DTYPES[dtype], device="cuda")
+                view = flat[at:at + rows * stride].view(rows, stride)[:, :vocab]
+                view.copy_(x)
+                got = ps.sample_logits(view, u, 0.9, 30, 0.95)
+                assert all(torch.equal(a, b) for a, b in zip(got, want)), (dtype, vocab, stride)
+
+
+def test_a_large_vocabulary():
+    n = (1 << 24) - 3
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    x = (torch.randn((1, n), generator=gen, device="cuda") * 2).bfloat16()
+    for s in ({}, {"top_p": 0.9}, {"top_k": 100}, {"min_p": 0.01}):
+        check(x.cpu(), uniform(1, 16), **s)
