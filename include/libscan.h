@@ -447,8 +447,11 @@ typedef struct {
  * The recurrence over the tokens t of each sequence and head,
  *     S(t) = e^g S(t - 1) + k(t) v(t)^T,    out(t) = scale S(t)^T q(t),
  * a prefix scan of (decay, key_width x value_width matrix) pairs, in its
- * chunked form.  Sums are held in 32 bits; bf16 rows are multiplied as bf16,
- * with the decayed scores and the state that a row reads rounded to bf16.
+ * chunked form.  Sums and states are held in 32 bits.  bf16 rows are
+ * multiplied as bf16, with the decayed scores and the state that a row reads
+ * rounded to bf16; f16 rows as the sums of two bf16 parts, scores and state
+ * rounded to two parts (2^-16).  State updates keep 24 bits of each decayed
+ * row (16 where no final state is asked for).
  *
  * state      device, [seqs][heads][key_width][value_width] floats: S before
  *            the first token, or NULL for zeros.

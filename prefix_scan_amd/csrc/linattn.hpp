@@ -48,6 +48,7 @@ struct Sweep {
     int m, n;
     int rev, shift;
     int out_f32;                 // out holds floats (partial gradients of shared heads)
+    int out_aligned;             // its rows start on 16 bytes and are whole multiples of them
     float pair_scale, out_scale;
     const float *state_in;       // per (sequence, head) m * n floats, or null
     float *state_out;
@@ -76,6 +77,10 @@ uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg
 size_t linattn_state_floats(int width);
 
 hipError_t launch_sweeps(const SweepSet &set, hipStream_t stream);
+// What launch_sweeps takes for bf16 and f16 rows, and the scan of segment
+// states (padded to `width` x `width`) that every kind of sweep shares.
+void launch_sweeps_split(const SweepSet &set, int width, hipStream_t stream);
+void launch_segment_scan(const SweepSet &set, int width, hipStream_t stream);
 
 // Sums the `share` consecutive heads of float rows into rows of `dtype`.
 struct HeadSum {
@@ -127,6 +132,13 @@ __device__ __forceinline__ Power decay_power(float g, double n)
 __device__ __forceinline__ float decayed(float x, Power p)
 {
     return __builtin_fmaf(x, p.hi, x * p.lo);
+}
+
+template <class T>
+__device__ __forceinline__ const T *row_ptr(const Rows &r, uint64_t seq, uint64_t tok, uint32_t head)
+{
+    return static_cast<const T *>(r.p) + (int64_t)seq * r.seq + (int64_t)tok * r.tok +
+           (int64_t)(head / r.share) * r.head;
 }
 
 // Which sequence, and which segment of it, a workgroup has.

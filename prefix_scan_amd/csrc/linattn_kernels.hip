@@ -83,13 +83,6 @@ __device__ __forceinline__ bool load_rows(const T *base, int64_t step, int cnt, 
     return bad;
 }
 
-template <class T>
-__device__ __forceinline__ const T *row_ptr(const Rows &r, uint64_t seq, uint64_t tok, uint32_t head)
-{
-    return static_cast<const T *>(r.p) + (int64_t)seq * r.seq + (int64_t)tok * r.tok +
-           (int64_t)(head / r.share) * r.head;
-}
-
 // STATES: only the segment's own contribution to the state, into set.seg.
 template <class T, int D, bool VEC, bool STATES>
 __global__ __launch_bounds__(D * 2) void sweep_f32_kernel(const SweepSet set)
@@ -434,28 +427,12 @@ void run_sweeps(const SweepSet &set, hipStream_t stream)
             sweep_f32_kernel<T, D, true, true><<<grid, D * 2, 0, stream>>>(set);
         else
             sweep_f32_kernel<T, D, false, true><<<grid, D * 2, 0, stream>>>(set);
-        segment_scan_kernel<D><<<dim3(D * D / 1024 * set.seqs, set.heads, (unsigned)set.count), 256, 0,
-                                 stream>>>(set);
+        launch_segment_scan(set, D, stream);
     }
     if (set.aligned)
         sweep_f32_kernel<T, D, true, false><<<grid, D * 2, 0, stream>>>(set);
     else
         sweep_f32_kernel<T, D, false, false><<<grid, D * 2, 0, stream>>>(set);
-}
-
-template <class T>
-hipError_t sweeps_of(const SweepSet &set, hipStream_t stream)
-{
-    int width = 0;
-    for (int i = 0; i < set.count; ++i) {
-        width = set.s[i].m > width ? set.s[i].m : width;
-        width = set.s[i].n > width ? set.s[i].n : width;
-    }
-    if (width <= 64)
-        run_sweeps<T, 64>(set, stream);
-    else
-        run_sweeps<T, 128>(set, stream);
-    return hipGetLastError();
 }
 
 template <class T>
@@ -499,13 +476,30 @@ uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg
     return ragged ? seqs + tokens / seg_len : seqs * ((tokens + seg_len - 1) / seg_len);
 }
 
+void launch_segment_scan(const SweepSet &set, int width, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(width * width / 1024) * set.seqs, set.heads, (unsigned)set.count);
+    if (width == 64)
+        segment_scan_kernel<64><<<grid, 256, 0, stream>>>(set);
+    else
+        segment_scan_kernel<128><<<grid, 256, 0, stream>>>(set);
+}
+
 hipError_t launch_sweeps(const SweepSet &set, hipStream_t stream)
 {
-    switch (set.dtype) {
-    case LIBSCAN_F32: return sweeps_of<float>(set, stream);
-    case LIBSCAN_BF16: return sweeps_of<__bf16>(set, stream);
-    default: return sweeps_of<_Float16>(set, stream);
+    int width = 0;
+    for (int i = 0; i < set.count; ++i) {
+        width = set.s[i].m > width ? set.s[i].m : width;
+        width = set.s[i].n > width ? set.s[i].n : width;
     }
+    width = width <= 64 ? 64 : 128;
+    if (set.dtype != LIBSCAN_F32)
+        launch_sweeps_split(set, width, stream);
+    else if (width == 64)
+        run_sweeps<float, 64>(set, stream);
+    else
+        run_sweeps<float, 128>(set, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_head_sum(const HeadSum &h, hipStream_t stream)
