@@ -32,6 +32,9 @@ namespace libscan {
 
 constexpr int kMaxSweeps = 3;
 constexpr int kLinattnWidth = 128;      // largest m and n
+// A segment of a sequence of no more than these adds up the states of those
+// before it by itself: cheaper than the scan's own launch and second pass.
+constexpr uint64_t kFewSegments = 4;
 
 // Rows of one tensor: token t of sequence s, head h starts at element
 // s * seq + t * tok + (h / share) * head.

@@ -1,32 +1,49 @@
-// linattn_split.hip -- the sweep of linattn.hpp for bf16 and f16 rows, in
-// bf16 matrix products (v_mfma_f32_32x32x16_bf16) with 32-bit sums.
+// linattn_split.hip -- the sweep of linattn.hpp in 16-bit matrix products
+// (v_mfma_f32_16x16x32) with 32-bit sums.
 //
-// A workgroup of D / 32 waves (D = 64 or 128) has one segment of one sequence
-// and head; wave w owns 32 columns n and keeps its m x 32 part of the state Z
-// in 32-bit accumulators for the whole segment.  It takes C = 64 tokens at a
-// time; with A, B, C the chunk's rows
+// A workgroup of D / 16 waves (D = 64 or 128) has one segment of one sequence
+// and head; wave w owns 16 columns n and keeps its m x 16 part of the state Z
+// in 32-bit accumulators for the whole segment.  It takes C tokens at a time
+// (64; 32 for f32 rows); with A, B, C the chunk's rows
 //
 //   out^T = Z^T A^T (p^(i+1-shift)) + C^T ((A B^T) o mask p^(i-j))^T
-//   Z    <- p^64 Z + B^T (p^(63+shift-j) C)
+//   Z    <- p^C Z + B^T (p^(C-1+shift-j) C)
 //
 // so the state is read and written once a segment and every row of a, b and
 // c is read once.  The rows of chunk t + 1 are on their way in registers
-// while chunk t is computed from LDS.
+// while chunk t is computed from LDS.  16 columns a wave keep it at 128
+// registers, so that four waves a SIMD hide each other's waits: with 32
+// columns and two waves the same chunks took 1.5 times as long.
 //
-// How exact.  A bf16 operand is one bf16 part, an f16 one the exact sum of
-// two (so that neither scores nor states can overflow f16).  The products
-// that feed the 16-bit outputs round their computed operand (scores, state)
-// to as many parts: one rounding of 2^-8 for bf16, of 2^-16 for f16.  The
-// state itself is a 32-bit sum of p^.. C split into three parts, exact to
-// 24 bits, times the exact B; where no state is asked for, and it is only
-// read through a rounding to the rows' own precision, two parts (2^-16) do.
+// How exact.  An operand is one or more 16-bit parts whose products are
+// summed in 32 bits:
+//   bf16 rows  are one part.  Scores and the state that a row reads are
+//              rounded to one (2^-8); the decayed rows that the state sums
+//              are cut into three, 24 bits, or two (2^-16) where no final
+//              state is asked for and the state is only read rounded.
+//   f16 rows   are one part of f16.  Scores, state and decayed rows leave
+//              f16's range, so each is scaled by a power of two taken from a
+//              bound of the chunk (largest exponents of its a, b and c; the
+//              state's bound follows its recurrence) and scaled back in 32
+//              bits; they are two parts each (2^-22).
+//   f32 rows   are three bf16 parts, 24 bits, as are scores, state and
+//              decayed rows; of the nine products the six above 2^-24 are
+//              taken, at a rate 2.7 times the 32-bit products'.
 //
-// Layouts.  An operand lane holds 8 consecutive k of row lane % 32, k from
-// 8 (lane / 32); an accumulator register r holds row 8 (r / 4) + 4 (lane /
-// 32) + r % 4 of column lane % 32.  C and B are read down their columns by
-// transposing LDS loads; for B these fetch the middle two of every four
-// groups of 4 columns the other way round, which makes the accumulators of Z
-// hold 8 consecutive m a lane: the second operand of Z^T A^T as they stand.
+// Layouts.  An operand lane holds 8 k of row lane % 16; an accumulator
+// register r holds row 4 (lane / 16) + r of column lane % 16.  C and B are
+// read down their columns by transposing LDS loads.  k runs in the order
+// that two tiles' accumulators have it, over the m and over the tokens of
+// every 32: lane group g has 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3.  So
+// the accumulators of Z are the operand of Z^T A^T as they stand, and the
+// column reads of b and c go through 16 rows on end.  Rows of a and of the
+// scores are stored in that order and 8 elements longer than they need be,
+// those of b and c 16: no read meets a bank twice.
+//
+// The chunk is causal by selection, not by multiplication: a masked pair is
+// zero whatever the product was.  A value that is not finite would still
+// reach earlier rows as 0 * inf, so a chunk with one is taken again one token
+// at a time.
 #include "linattn.hpp"
 
 #include "../../include/libscan.h"
@@ -36,31 +53,46 @@ namespace libscan {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int C = 64;                   // tokens of a chunk
-
+// Parts of a row's elements, and of scores and the state where they are
+// multiplied.
 template <class T>
 struct In;
 template <>
 struct In<__bf16> {
-    static constexpr int kParts = 1;
-    static constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+    static constexpr int kParts = 1, kMade = 1, kChunk = 64;
+    static constexpr bool kScaled = false;
 };
 template <>
 struct In<_Float16> {
-    static constexpr int kParts = 2;
-    static constexpr uint32_t kExp = 0x7C007C00u, kOne = 0x04000400u;
+    static constexpr int kParts = 1, kMade = 2, kChunk = 64;
+    static constexpr bool kScaled = true;
+};
+template <>
+struct In<float> {
+    static constexpr int kParts = 3, kMade = 3, kChunk = 32;
+    static constexpr bool kScaled = false;
 };
 
 __device__ __forceinline__ float low16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float above(float x) { return high16(__float_as_uint(x)); }
+
+template <bool F16>
+__device__ __forceinline__ float value16(uint32_t w, int high)
+{
+    if constexpr (F16)
+        return (float)__builtin_bit_cast(f16x2, w)[high];
+    else
+        return high ? high16(w) : low16(w);
+}
 
 // Two floats' upper halves in one word: both cut to bf16.
 __device__ __forceinline__ uint32_t cut_pair(float a, float b)
@@ -68,151 +100,321 @@ __device__ __forceinline__ uint32_t cut_pair(float a, float b)
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
+template <bool F16>
 __device__ __forceinline__ uint32_t round_pair(float a, float b)
 {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+    if constexpr (F16)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, f16x2));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-__device__ __forceinline__ float above(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
-
-// What is left of x past its part h, and nothing where x is not finite.
+// What is left of x past its part h; some number where x is not finite, so
+// that the parts' sum stays what x is.
+template <bool F16, bool FINITE>
 __device__ __forceinline__ float rest(float x, float h)
 {
-    return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u ? 0.f : x - h;
+    constexpr float most = F16 ? 32768.f : 0x1p126f;
+    if constexpr (FINITE)
+        return x - h;
+    return __builtin_amdgcn_fmed3f(x - h, -most, most);
 }
 
-// Eight floats in P parts, each rounded to nearest from what the ones before
-// it left.
-template <int P, bool FINITE>
-__device__ __forceinline__ void parts_of(const float *x, u32x4 *out)
+// Two floats in P parts: bf16 ones are cut but for the last, which is rounded
+// to nearest from what they left; f16 ones are rounded.
+template <int P, bool F16, bool FINITE>
+__device__ __forceinline__ void parts_of_pair(float a, float b, uint32_t *out)
 {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float a = x[2 * e], b = x[2 * e + 1];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            if (p + 1 == P) {
-                out[p][e] = round_pair(a, b);
-            } else if (FINITE) {
-                out[p][e] = cut_pair(a, b);
-                a -= above(a);
-                b -= above(b);
-            } else {
-                const uint32_t w = round_pair(a, b);
-                out[p][e] = w;
-                a = rest(a, low16(w));
-                b = rest(b, high16(w));
+    for (int p = 0; p < P; ++p) {
+        if (p + 1 == P || F16) {
+            out[p] = round_pair<F16>(a, b);
+            if (p + 1 < P) {
+                a = rest<F16, FINITE>(a, value16<F16>(out[p], 0));
+                b = rest<F16, FINITE>(b, value16<F16>(out[p], 1));
             }
+        } else {
+            out[p] = cut_pair(a, b);
+            a = rest<F16, FINITE>(a, above(a));
+            b = rest<F16, FINITE>(b, above(b));
         }
     }
 }
 
-// This thread's 16 bytes of rows [0, cnt) of a chunk, zeros past them.
+template <int P, bool F16, bool FINITE>
+__device__ __forceinline__ void parts_of(const float *x, u32x4 *out)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t w[P];
+        parts_of_pair<P, F16, FINITE>(x[2 * e], x[2 * e + 1], w);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            out[p][e] = w[p];
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c)
+{
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// The same number, which the compiler takes for a new one: what follows from
+// it stays where it is, instead of in registers all through the loop.
+__device__ __forceinline__ int afresh(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// A number that all lanes have, in a scalar register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t x)
+{
+    return (uint64_t)uniform((uint32_t)(x >> 32)) << 32 | uniform((uint32_t)x);
+}
+
+__device__ __forceinline__ float uniform_float(float x) { return __uint_as_float(uniform(__float_as_uint(x))); }
+
+__device__ __forceinline__ double uniform_double(double x)
+{
+    return __longlong_as_double((int64_t)uniform64((uint64_t)__double_as_longlong(x)));
+}
+
+// Eight elements of a row, as fetched.
+template <class T>
+struct Unit {
+    u32x4 w[sizeof(T) / 2];
+};
+
+// This thread's units of rows [0, cnt) of a chunk, zeros past them.
 template <class T, bool VEC, int W, int THREADS, int N>
-__device__ __forceinline__ void fetch(u32x4 (&r)[N], const T *base, int64_t step, int cnt, int width)
+__device__ __forceinline__ void fetch(Unit<T> (&r)[N], const T *base, int64_t step, int cnt, int width)
 {
     constexpr int PER = W / 8, RS = THREADS / PER;
-    static_assert(N == C / RS, "a chunk of C rows");
-    const int row0 = threadIdx.x / PER, col = threadIdx.x % PER * 8;
+    static_assert(N == In<T>::kChunk / RS, "a chunk of rows");
+    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, col = tid % PER * 8;
     const T *p = base + row0 * step + col;
+    if (VEC && cnt == In<T>::kChunk && width == W) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+#pragma unroll
+            for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                r[k].w[h] = reinterpret_cast<const u32x4 *>(p)[h];
+            p += RS * step;
+        }
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        r[k] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+            r[k].w[h] = u32x4{0, 0, 0, 0};
         if (row0 + k * RS < cnt && col < width) {
             if (VEC) {
-                r[k] = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+                for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                    if (h == 0 || col + 4 < width)
+                        r[k].w[h] = reinterpret_cast<const u32x4 *>(p)[h];
+            } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < width)
+                        r[k].w[e / 4][e % 4] = __float_as_uint(p[e]);
             } else {
                 const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (col + e < width)
-                        r[k][e / 2] |= (uint32_t)h[e] << (16 * (e & 1));
+                        r[k].w[0][e / 2] |= (uint32_t)h[e] << (16 * (e & 1));
             }
         }
         p += RS * step;
     }
 }
 
-// The fetched rows into LDS, split into parts.
-template <class T, int W, int THREADS, int N, int LD>
-__device__ __forceinline__ void stage(const u32x4 (&r)[N], __bf16 (*dst)[C][LD])
+// The fetched rows into LDS, in parts; PERMUTED in the order of k.
+template <class T, bool PERMUTED, int W, int THREADS, int N, int CH, int LD>
+__device__ __forceinline__ void stage(const Unit<T> (&r)[N], uint16_t (*dst)[CH][LD])
 {
     constexpr int PER = W / 8, RS = THREADS / PER;
-    const int row0 = threadIdx.x / PER, col = threadIdx.x % PER * 8;
+    const int row0 = threadIdx.x / PER, unit = threadIdx.x % PER;
+    const int col = PERMUTED ? unit / 4 * 32 + (unit & 1) * 16 + (unit & 2) * 2 : unit * 8;
+    const auto put = [&](int part, int row, u32x4 w) {
+        uint16_t *p = &dst[part][row][col];
+        if (PERMUTED) {
+            *reinterpret_cast<u32x2 *>(p) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2 *>(p + 8) = u32x2{w[2], w[3]};
+        } else {
+            *reinterpret_cast<u32x4 *>(p) = w;
+        }
+    };
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        if constexpr (In<T>::kParts == 1) {
-            *reinterpret_cast<u32x4 *>(&dst[0][row0 + k * RS][col]) = r[k];
+        if constexpr (sizeof(T) == 2) {
+            put(0, row0 + k * RS, r[k].w[0]);
         } else {
-            typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-            const f16x8 h = __builtin_bit_cast(f16x8, r[k]);
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[e] = (float)h[e];
-            u32x4 p[In<T>::kParts];
-            parts_of<In<T>::kParts, false>(x, p);
+                x[e] = __uint_as_float(r[k].w[e / 4][e % 4]);
+            u32x4 p[3];
+            parts_of<3, false, false>(x, p);
 #pragma unroll
-            for (int i = 0; i < In<T>::kParts; ++i)
-                *reinterpret_cast<u32x4 *>(&dst[i][row0 + k * RS][col]) = p[i];
+            for (int i = 0; i < 3; ++i)
+                put(i, row0 + k * RS, p[i]);
         }
     }
 }
 
 template <class T, int N>
-__device__ __forceinline__ bool any_not_finite(const u32x4 (&r)[N])
+__device__ __forceinline__ bool any_not_finite(const Unit<T> (&r)[N])
 {
     uint32_t bad = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            bad |= ((r[k][e] & In<T>::kExp) + In<T>::kOne) & 0x80008000u;
-    return bad != 0;
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = r[k].w[h][e];
+                if constexpr (sizeof(T) == 4)
+                    bad |= (w & 0x7F800000u) + 0x00800000u;
+                else
+                    bad |= (w & 0x7F807F80u) + 0x00800080u;
+            }
+    return (bad & (sizeof(T) == 4 ? 0x80000000u : 0x80008000u)) != 0;
 }
 
-// Eight rows down 16 columns: p is this lane's place in the first four.
+// The largest of a wave's numbers in [0, 2 TOP).
+template <int TOP>
+__device__ __forceinline__ int wave_most(int own)
+{
+    int most = 0;
+#pragma unroll
+    for (int b = TOP; b; b >>= 1)
+        if (__any(own >= most + b))
+            most += b;
+    return most;
+}
+
+// The largest biased exponent among a wave's f16 values (31: not finite).
+template <class T, int N>
+__device__ __forceinline__ int wave_exponent(const Unit<T> (&r)[N])
+{
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t l = r[k].w[0][e] & 0x7C00u, h = r[k].w[0][e] & 0x7C000000u;
+            lo = l > lo ? l : lo;
+            hi = h > hi ? h : hi;
+        }
+    lo >>= 10;
+    hi >>= 26;
+    const int own = (int)(lo > hi ? lo : hi);
+    return wave_most<16>(own);
+}
+
+// LDS by its own pointers: a lane's place plus a constant, which the
+// instruction adds.
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
+// Eight rows down 16 columns, in the order of k: p is this lane's place in
+// the first four of them.
 template <int LD>
-__device__ __forceinline__ u32x4 column_frag(const __bf16 *p)
+__device__ __forceinline__ u32x4 column_frag(lds_u16 *p)
 {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
     const u32x2 b = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * LD)));
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * LD)));
     return u32x4{a[0], a[1], b[0], b[1]};
 }
 
-__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c)
+__device__ __forceinline__ u32x4 row_frag(lds_u16 *p)
 {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    return *(const __attribute__((address_space(3))) u32x4 *)p;
 }
 
-template <int D, int IP, bool STATES>
+// The same of a row that is not stored in the order of k.
+__device__ __forceinline__ u32x4 row_frag_of(lds_u16 *p)
+{
+    typedef const __attribute__((address_space(3))) u32x2 lds_u32x2;
+    const u32x2 a = *(lds_u32x2 *)p, b = *(lds_u32x2 *)(p + 16);
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+__device__ __forceinline__ float power2(int e)
+{
+    return __builtin_amdgcn_ldexpf(1.f, e < -120 ? -120 : e > 120 ? 120 : e);
+}
+
+// e with |x| < 2^e.
+__device__ __forceinline__ int above_exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 126; }
+
+// This lane's row and four of the 16 columns from `first` of each tile.
+template <class T, int IT>
+__device__ __forceinline__ void put_out(const f32x4 *o, T *out, int64_t step, int cnt, int first, int n,
+                                        bool aligned)
+{
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    const int lane = afresh((int)threadIdx.x & 63), row = lane & 15, c0 = first + lane / 16 * 4;
+    if (aligned && cnt == 16 * IT) {
+        T *to = out + row * step + c0;
+        if (c0 < n) {
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                *reinterpret_cast<t4 *>(to) = __builtin_convertvector(o[it], t4);
+                to += 16 * step;
+            }
+        }
+        return;
+    }
+    T *to = out + row * step + c0;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (16 * it + row < cnt && c0 + e < n)
+                to[e] = (T)o[it][e];
+        to += 16 * step;
+    }
+}
+
+template <class T, int D, bool STATES>
 struct Lds {
-    static constexpr int LD = D + 16;      // 16 B apart in bank: rows and columns both read clean
-    static constexpr int LP = C + 8;
-    union {
-        __bf16 a[STATES ? 1 : IP][STATES ? 1 : C][LD];
-        __bf16 o[STATES ? 1 : D / 32][STATES ? 1 : C][32];      // a wave's outputs, once a is read
-    };
-    __bf16 b[IP][C][LD];
-    __bf16 c[IP][C][LD];
-    __bf16 p[STATES ? 1 : IP][STATES ? 1 : C][LP];
-    float pw[C + 8], pl[C + 8];            // powers of the decay: hi, lo
-    float pair[C + 32];                    // pair_scale p^d at 31 + d
+    static constexpr int C = In<T>::kChunk, IP = In<T>::kParts, OP = In<T>::kMade;
+    static constexpr int LA = D + 8, LD = D + 16, LP = C + 8;
+    uint16_t a[STATES ? 1 : IP][STATES ? 1 : C][LA];
+    uint16_t b[IP][C][LD];
+    uint16_t c[IP][C][LD];
+    uint16_t p[STATES ? 1 : OP][STATES ? 1 : C][LP];
+    float pw[C + 4], pl[C + 4];            // powers of the decay: hi, lo
+    float pair[C + 16];                    // pair_scale p^d at 16 + d, 0 for d < 0
     float wt[C];                           // pair_scale p^(cnt-1+shift-j)
     int bad[2];
+    int exponent[2][4];                    // of a, b, c
 };
 
 // STATES: only the segment's own contribution to the state, into set.seg.
 // WP: parts of the decayed rows that the state sums.
 template <class T, int D, bool VEC, int WP, bool STATES>
-__global__ __launch_bounds__(D * 2, In<T>::kParts == 1 ? 2 : 1) void sweep_split_kernel(const SweepSet set)
+__global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void sweep_split_kernel(const SweepSet set)
 {
-    constexpr int NW = D / 32, THREADS = D * 2, MT = D / 32, IP = In<T>::kParts;
+    constexpr int C = In<T>::kChunk, IP = In<T>::kParts, OP = In<T>::kMade;
+    constexpr int NW = D / 16, THREADS = D * 4, KK = D / 32, IT = C / 16, KS = C / 32;
     constexpr int N = C * D / 8 / THREADS;
-    typedef Lds<D, IP, STATES> S;
+    constexpr bool F16 = In<T>::kScaled;
+    typedef Lds<T, D, STATES> S;
     __shared__ __align__(16) S s;
 
     const Sweep &sw = set.s[blockIdx.z];
@@ -220,58 +422,104 @@ __global__ __launch_bounds__(D * 2, In<T>::kParts == 1 ? 2 : 1) void sweep_split
     Place pl;
     if (!place_of(set, blockIdx.x, &pl))
         return;
+    pl.seq = uniform(pl.seq);
+    pl.first = uniform64(pl.first);
+    pl.len = uniform64(pl.len);
+    pl.lo = uniform64(pl.lo);
+    pl.hi = uniform64(pl.hi);
+    pl.last = pl.hi == pl.len;
     if (STATES && pl.last)
         return;
-    const int wave = threadIdx.x / 64, lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+    const int wave = uniform(threadIdx.x / 64);
+    const int lane = threadIdx.x & 63, g4 = lane >> 4, l16 = lane & 15;
     const float g = set.log_decay[head];
-    for (int i = threadIdx.x; i < C + 2; i += THREADS) {
-        const Power p = decay_power(g, (double)i);
-        s.pw[i] = p.hi;
-        s.pl[i] = p.lo;
+    const int m = sw.m, n = sw.n;
+    for (int i = threadIdx.x; i < C + 17; i += THREADS) {
+        const int d = i - 16;
+        const Power p = d >= 0 ? decay_power(g, (double)d) : Power{0.f, 0.f};
+        if (d < C)
+            s.pair[i] = sw.pair_scale * p.hi;
+        if (d >= 0) {
+            s.pw[d] = p.hi;
+            s.pl[d] = p.lo;
+        }
     }
-    if (threadIdx.x < C + 31) {
-        const int d = (int)threadIdx.x - 31;
-        s.pair[threadIdx.x] = d >= 0 ? sw.pair_scale * decay_power(g, (double)d).hi : 0.f;
-    }
-    if (threadIdx.x < 2)
+    if (threadIdx.x < 2) {
         s.bad[threadIdx.x] = 0;
+        for (int i = 0; i < 4; ++i)
+            s.exponent[threadIdx.x][i] = 0;
+    }
+    if constexpr (!STATES)                  // the scores' upper corner stays zero
+        for (int i = threadIdx.x; i < OP * C * S::LP; i += THREADS)
+            (&s.p[0][0][0])[i] = 0;
 
-    const int m = sw.m, n = sw.n, col = wave * 32 + l32;
+    const int col = wave * 16 + l16;
+    const bool active = wave * 16 < n;      // whether the wave has columns
     const uint64_t sh = (uint64_t)pl.seq * set.heads + head;
-    float *seg = set.seg + (((uint64_t)blockIdx.z * set.items + blockIdx.x) * set.heads + head) *
-                               (D * D) + wave * (MT * 16 * 64) + lane;
-    // z[mt][r]: row 32 mt + 16 (r / 8) + 8 half + r % 8 of column col.
-    f32x16 z[MT];
+    // Two tiles of 16 rows: z[kk][u][r] is row 32 kk + 16 u + 4 g4 + r of column col.
+    f32x4 z[KK][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-            z[mt][r] = 0.f;
-    if (!STATES) {
-        if (pl.lo)
+        for (int u = 0; u < 2; ++u)
+            z[kk][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const auto seg_of = [&](uint32_t item) {
+        return set.seg + (((uint64_t)blockIdx.z * set.items + item) * set.heads + head) * (D * D) +
+               (wave * KK * 64 + lane) * 8;
+    };
+    if (!STATES && active) {
+        if (pl.lo) {
+            // The scan's result, or the scan itself where segments are few.
+            const bool few = pl.len <= kFewSegments * set.seg_len;
+            const uint32_t before = few ? (uint32_t)(pl.lo / set.seg_len) : 1;
+            const Power w = decay_power(g, (double)set.seg_len);
+            for (uint32_t k = 0; k < before; ++k) {
+                const float *seg = seg_of(few ? blockIdx.x - before + k : blockIdx.x);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    z[mt][r] = seg[(mt * 16 + r) * 64];
+                    for (int u = 0; u < 2; ++u) {
+                        const f32x4 t = *reinterpret_cast<const f32x4 *>(seg + kk * 512 + 4 * u);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            z[kk][u][r] = decayed(z[kk][u][r], w) + t[r];
+                    }
+            }
+        }
         if (sw.state_in && col < n) {
             const Power w = decay_power(g, (double)pl.lo);
             const float *st = sw.state_in + sh * ((uint64_t)m * n) + col * sw.state_n;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = mt * 32 + 16 * (r / 8) + 8 * half + r % 8;
+                for (int e = 0; e < 8; ++e) {
+                    const int row = kk * 32 + e / 4 * 16 + 4 * g4 + e % 4;
                     if (row < m)
-                        z[mt][r] += decayed(st[row * sw.state_m], w);
+                        z[kk][e / 4][e % 4] += decayed(st[row * sw.state_m], w);
                 }
         }
     }
+    // f16: z holds the state times 2^sigma, whose absolute values are below bound.
+    int sigma = 0;
+    float bound = 0.f;
+    const auto find_bound = [&]() {
+        float own = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = __builtin_fabsf(z[kk][e / 4][e % 4]);
+                own = x > own && x < __builtin_inff() ? x : own;
+            }
+        bound = power2(wave_most<128>(own > 0.f ? above_exponent(own) + 126 : 0) - 126 - sigma);
+    };
+    if constexpr (F16 && !STATES)
+        find_bound();
 
     const int64_t dir = sw.rev ? -1 : 1;
     const T *pa = row_ptr<T>(sw.a, pl.seq, 0, head), *pb = row_ptr<T>(sw.b, pl.seq, 0, head),
             *pc = row_ptr<T>(sw.c, pl.seq, 0, head);
-    u32x4 ra[STATES ? 1 : N], rb[N], rc[N];
+    Unit<T> ra[STATES ? 1 : N], rb[N], rc[N];
     const auto fetch_chunk = [&](uint64_t at, int cnt) {
         const int64_t tok = (int64_t)(pl.first + (sw.rev ? pl.len - 1 - at : at));
         if constexpr (!STATES)
@@ -279,37 +527,63 @@ __global__ __launch_bounds__(D * 2, In<T>::kParts == 1 ? 2 : 1) void sweep_split
         fetch<T, VEC, D, THREADS>(rb, pb + tok * sw.b.tok, dir * sw.b.tok, cnt, m);
         fetch<T, VEC, D, THREADS>(rc, pc + tok * sw.c.tok, dir * sw.c.tok, cnt, n);
     };
-
-    // The scores' tile of this wave (rows ti, columns tj of the 2 x 2; the
-    // fourth is all masked).  With two waves the first has both on the diagonal.
-    const int ti = NW == 4 ? (wave != 0) : wave, tj = NW == 4 ? wave == 2 : 0;
-    // Places of this lane in column reads: row (of 16) and column.
-    const int trow = 8 * half + (lane & 15) / 4, tcol = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-    const int tswap = 16 * ((lane >> 4) & 1) + 4 * ((lane & 3) == 1 ? 2 : (lane & 3) == 2 ? 1 : lane & 3);
+    // This lane's places: along the rows of a, b and the scores, and down the
+    // columns of b and c.
+    lds_u16 *const arow = (lds_u16 *)&s.a[0][0][0] + l16 * S::LA + 8 * g4;
+    lds_u16 *const bcol = (lds_u16 *)&s.b[0][0][0] + (4 * g4 + l16 / 4) * S::LD + 4 * (l16 & 3);
+    lds_u16 *const ccol = (lds_u16 *)&s.c[0][0][0] + (4 * g4 + l16 / 4) * S::LD + 4 * (l16 & 3) + wave * 16;
 
     uint64_t at = pl.lo, single = 0;   // tokens below `single` are taken one at a time
     int cnt = pl.hi - at < C ? (int)(pl.hi - at) : C, cnt_wt = -1, turn = 0;
+    double whole = 1.0, drift = 1.0;   // p^cnt; what the factors so far left of it
+    float wt_max = 0.f, wt_sum = 0.f;
     fetch_chunk(at, cnt);
     while (at < pl.hi) {
         __syncthreads();
         if constexpr (!STATES)
-            stage<T, D, THREADS>(ra, s.a);
-        stage<T, D, THREADS>(rb, s.b);
-        stage<T, D, THREADS>(rc, s.c);
-        if (__any(any_not_finite<T>(rc)) && lane == 0)
-            s.bad[turn] = 1;
+            stage<T, true, D, THREADS>(ra, s.a);
+        stage<T, false, D, THREADS>(rb, s.b);
+        stage<T, false, D, THREADS>(rc, s.c);
+        if constexpr (F16) {
+            int e[3] = {0, wave_exponent(rb), wave_exponent(rc)};
+            if constexpr (!STATES)
+                e[0] = wave_exponent(ra);
+            if (lane < 3)
+                atomicMax(&s.exponent[turn][lane], lane == 0 ? e[0] : lane == 1 ? e[1] : e[2]);
+        } else {
+            if (__any(any_not_finite(rc)) && lane == 0)
+                s.bad[turn] = 1;
+        }
         if (cnt != cnt_wt) {
-            if (threadIdx.x < C) {
-                const int j = threadIdx.x;
+            const int j = afresh((int)threadIdx.x);
+            if (j < C)
                 s.wt[j] = j < cnt ? sw.pair_scale * s.pw[cnt - 1 + sw.shift - j] : 0.f;
+            if constexpr (F16) {
+                // Their largest, and a bound of their sum.
+                wt_max = uniform_float(__builtin_fabsf(sw.pair_scale) *
+                                       fmaxf(s.pw[cnt - 1 + sw.shift], s.pw[sw.shift]));
+                const float far = 1.f / (1.f - s.pw[1]);
+                wt_sum = uniform_float(wt_max * (far > 0.f && far < cnt ? far : (float)cnt));
             }
             cnt_wt = cnt;
+            whole = uniform_double((double)s.pw[cnt] + (double)s.pl[cnt]);
         }
         __syncthreads();
-        const bool bad = s.bad[turn] != 0;
+        int ea = 0, eb = 0, ec = 0;
+        bool bad;
+        if constexpr (F16) {
+            ea = (int)uniform(s.exponent[turn][0]);
+            eb = (int)uniform(s.exponent[turn][1]);
+            ec = (int)uniform(s.exponent[turn][2]);
+            bad = ea == 31 || eb == 31 || ec == 31;
+        } else {
+            bad = uniform(s.bad[turn]) != 0;
+        }
         turn ^= 1;
         if (threadIdx.x == 0)
             s.bad[turn] = 0;
+        if (F16 && threadIdx.x < 3)
+            s.exponent[turn][threadIdx.x] = 0;
         if (bad && cnt > 1) {          // again, one token at a time
             single = at + cnt;
             cnt = 1;
@@ -322,246 +596,231 @@ __global__ __launch_bounds__(D * 2, In<T>::kParts == 1 ? 2 : 1) void sweep_split
         if (next_cnt)
             fetch_chunk(next, next_cnt);
 
-        f32x16 o[2];
+        // f16: scores are scaled by 2^rho, the state that is read by 2^tau.
+        int rho = 0, tau = 0;
+        if constexpr (F16) {
+            const float most = fmaxf(__builtin_fabsf(s.pair[16]), __builtin_fabsf(s.pair[16 + C - 1]));
+            rho = 15 - (ea + eb - 28 + 7 + (int)uniform((uint32_t)above_exponent(most)));
+            rho = rho < -40 ? -40 : rho > 40 ? 40 : rho;
+            tau = 15 - above_exponent(bound);
+        }
+        f32x4 o[IT];
         if constexpr (!STATES) {
-            // Scores, transposed: a lane has token i of its tile and four
-            // consecutive j at a time.
-            if (wave < 3) {
+            // Scores, transposed: a lane has token i and four consecutive j.
+            const int own = afresh(lane), oi = own & 15, og = own / 16;
+            lds_u16 *const brow = (lds_u16 *)&s.b[0][0][0] + oi * S::LD + 4 * og;
+#pragma unroll 1
+            for (int x = wave; x < IT * (IT + 1) / 2; x += NW) {
+                const int it = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, jt = x - it * (it + 1) / 2;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < (NW == 4 ? 1 : 2); ++k) {
-                    if (k && wave)
-                        break;
-                    const int it = ti + k, jt = tj + k;
-                    f32x16 acc;
+                for (int kk = 0; kk < KK; ++kk) {
+                    u32x4 af[IP], bf[IP];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        acc[r] = 0.f;
-#pragma unroll
-                    for (int q = 0; q < 2 * MT; ++q) {
-                        u32x4 af[IP], bf[IP];
-#pragma unroll
-                        for (int p = 0; p < IP; ++p) {
-                            af[p] = *reinterpret_cast<const u32x4 *>(&s.a[p][32 * it + l32][16 * q + 8 * half]);
-                            bf[p] = *reinterpret_cast<const u32x4 *>(&s.b[p][32 * jt + l32][16 * q + 8 * half]);
-                        }
-#pragma unroll
-                        for (int x = 0; x < IP; ++x)
-#pragma unroll
-                            for (int y = 0; x + y < IP; ++y)
-                                acc = mma(bf[x], af[y], acc);
+                    for (int p = 0; p < IP; ++p) {
+                        af[p] = row_frag(arow + (p * C + 16 * it) * S::LA + 32 * kk);
+                        bf[p] = row_frag_of(brow + (p * C + 16 * jt) * S::LD + 32 * kk);
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float x[4];
+                    for (int u = 0; u < IP; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int d = 32 * (ti - tj) + l32 - (8 * q + 4 * half + e);
-                            x[e] = acc[4 * q + e] * s.pair[31 + d];
-                            if (d < 0)
-                                x[e] = 0.f;
-                        }
-#pragma unroll
-                        for (int p = 0; p < IP; ++p) {
-                            const u32x2 w = {round_pair(x[0], x[1]), round_pair(x[2], x[3])};
-                            *reinterpret_cast<u32x2 *>(&s.p[p][32 * it + l32][32 * jt + 8 * q + 4 * half]) = w;
-                            if (p + 1 < IP) {
-                                x[0] = rest(x[0], low16(w[0]));
-                                x[1] = rest(x[1], high16(w[0]));
-                                x[2] = rest(x[2], low16(w[1]));
-                                x[3] = rest(x[3], high16(w[1]));
-                            }
-                        }
-                    }
+                        for (int v = 0; u + v < IP; ++v)
+                            acc = mma<F16>(bf[u], af[v], acc);
                 }
+                const int d0 = 16 * (it - jt) + oi - 4 * og;
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = acc[e] * s.pair[16 + d0 - e];
+                    if constexpr (F16)
+                        y[e] *= power2(rho);
+                    if (d0 - e < 0)
+                        y[e] = 0.f;
+                }
+                uint32_t w0[OP], w1[OP];
+                parts_of_pair<OP, F16, false>(y[0], y[1], w0);
+                parts_of_pair<OP, F16, false>(y[2], y[3], w1);
+#pragma unroll
+                for (int p = 0; p < OP; ++p)
+                    *reinterpret_cast<u32x2 *>(&s.p[p][16 * it + oi][32 * (jt / 2) + 8 * og + 4 * (jt & 1)]) = u32x2{w0[p], w1[p]};
             }
 
             // What the rows read of the state.
 #pragma unroll
-            for (int it = 0; it < 2; ++it)
+            for (int it = 0; it < IT; ++it)
+                o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (active) {
+                const float by = F16 ? power2(tau - sigma) : 1.f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    o[it][r] = 0.f;
+                for (int kk = 0; kk < KK; ++kk) {
+                    float x[8];
+                    u32x4 zf[OP];
 #pragma unroll
-            for (int q = 0; q < 2 * MT; ++q) {
-                float x[8];
-                u32x4 zf[IP];
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = F16 ? z[kk][e / 4][e % 4] * by : z[kk][e / 4][e % 4];
+                    parts_of<OP, F16, false>(x, zf);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[e] = z[q / 2][8 * (q % 2) + e];
-                parts_of<IP, false>(x, zf);
+                    for (int it = 0; it < IT; ++it)
 #pragma unroll
-                for (int it = 0; it < 2; ++it)
+                        for (int v = 0; v < IP; ++v) {
+                            const u32x4 af = row_frag(arow + (v * C + 16 * it) * S::LA + 32 * kk);
 #pragma unroll
-                    for (int y = 0; y < IP; ++y) {
-                        const u32x4 af = *reinterpret_cast<const u32x4 *>(
-                            &s.a[y][32 * it + l32][16 * q + 8 * half]);
+                            for (int u = 0; u + v < OP; ++u)
+                                o[it] = mma<F16>(zf[u], af, o[it]);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
-                        for (int w = 0; w + y < IP; ++w)
-                            o[it] = mma(zf[w], af, o[it]);
-                    }
-            }
+                for (int it = 0; it < IT; ++it) {
+                    float w = s.pw[16 * it + oi + 1 - sw.shift];
+                    if constexpr (F16)
+                        w = w * power2(rho - tau);
 #pragma unroll
-            for (int it = 0; it < 2; ++it) {
-                const float w = s.pw[32 * it + l32 + 1 - sw.shift];
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    o[it][r] *= w;
+                    for (int r = 0; r < 4; ++r)
+                        o[it][r] *= w;
+                }
             }
             __syncthreads();
         }
 
-        // What they read of the chunk's own tokens, and the state past it.
-        const Power whole = {s.pw[cnt], s.pl[cnt]};
+        // What they read of the chunk's own tokens.
+        if constexpr (!STATES) {
+            if (active) {
+                const int own = afresh(lane);
+                lds_u16 *const prow = (lds_u16 *)&s.p[0][0][0] + (own & 15) * S::LP + own / 16 * 8;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                z[mt][r] = decayed(z[mt][r], whole);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            u32x4 cf[IP];
-#pragma unroll
-            for (int p = 0; p < IP; ++p)
-                cf[p] = column_frag<S::LD>(&s.c[p][16 * q + trow][32 * wave + tcol]);
-            if constexpr (!STATES) {
-#pragma unroll
-                for (int it = q / 2; it < 2; ++it)
-#pragma unroll
-                    for (int y = 0; y < IP; ++y) {
-                        const u32x4 pf = *reinterpret_cast<const u32x4 *>(
-                            &s.p[y][32 * it + l32][16 * q + 8 * half]);
-#pragma unroll
-                        for (int x = 0; x + y < IP; ++x)
-                            o[it] = mma(cf[x], pf, o[it]);
-                    }
-            }
-            if (bad)
-                continue;
-            float x[8];
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&s.wt[16 * q + 8 * half]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&s.wt[16 * q + 8 * half + 4]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = e & 1 ? high16(cf[0][e / 2]) : low16(cf[0][e / 2]);
-#pragma unroll
-                for (int p = 1; p < IP; ++p)
-                    x[e] += e & 1 ? high16(cf[p][e / 2]) : low16(cf[p][e / 2]);
-                x[e] *= e < 4 ? w0[e] : w1[e - 4];
-            }
-            u32x4 xf[WP];
-            parts_of<WP, true>(x, xf);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int y = 0; y < IP; ++y) {
-                    const u32x4 bf = column_frag<S::LD>(&s.b[y][16 * q + trow][32 * mt + tswap]);
-#pragma unroll
-                    for (int p = 0; p + y < WP; ++p)
-                        z[mt] = mma(bf, xf[p], z[mt]);
-                }
-        }
-        if (bad) {                     // one token, with a value that is not finite
-            float v = 0.f;
-#pragma unroll
-            for (int p = 0; p < IP; ++p)
-                v += (float)s.c[p][0][col];
-            v *= s.wt[0];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float b = 0.f;
+                for (int ks = 0; ks < KS; ++ks) {
+                    u32x4 cf[IP];
 #pragma unroll
                     for (int p = 0; p < IP; ++p)
-                        b += (float)s.b[p][0][mt * 32 + 16 * (r / 8) + 8 * half + r % 8];
-                    z[mt][r] = __builtin_fmaf(b, v, z[mt][r]);
-                }
-        }
-
-        if constexpr (!STATES) {
-            const uint64_t t0 = pl.first + (sw.rev ? pl.len - 1 - at : at);
-            const int64_t row0 = (int64_t)pl.seq * sw.out_seq + (int64_t)t0 * sw.out_tok +
-                                 (int64_t)head * sw.out_head + wave * 32;
-            const int64_t step = dir * sw.out_tok;
-            if (sw.out_f32) {          // partial gradients of shared heads: dense, so aligned
-                float *out = static_cast<float *>(sw.out) + row0;
+                        cf[p] = column_frag<S::LD>(ccol + (p * C + 32 * ks) * S::LD);
 #pragma unroll
-                for (int it = 0; it < 2; ++it) {
-                    const int i = 32 * it + l32;
+                    for (int it = 2 * ks; it < IT; ++it)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        f32x4 y;
+                        for (int v = 0; v < OP; ++v) {
+                            const u32x4 pf = row_frag(prow + (v * C + 16 * it) * S::LP + 32 * ks);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = o[it][4 * q + e] * sw.out_scale;
-                        const int c0 = 8 * q + 4 * half;
-                        if (i >= cnt || wave * 32 + c0 >= n)
-                            continue;
-                        if (n % 4 == 0) {
-                            *reinterpret_cast<f32x4 *>(out + i * step + c0) = y;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (wave * 32 + c0 + e < n)
-                                    out[i * step + c0 + e] = y[e];
+                            for (int u = 0; u < IP && u + v < OP; ++u)
+                                o[it] = mma<F16>(cf[u], pf, o[it]);
                         }
-                    }
                 }
-            } else {
-                // Through LDS, in 16-byte pieces that trade places by row.
+                const uint64_t t0 = pl.first + (sw.rev ? pl.len - 1 - at : at);
+                const int64_t step = dir * sw.out_tok;
+                const int64_t row0 = (int64_t)pl.seq * sw.out_seq + (int64_t)t0 * sw.out_tok +
+                                     (int64_t)head * sw.out_head;
+                const float by = F16 ? sw.out_scale * power2(-rho) : sw.out_scale;
 #pragma unroll
-                for (int it = 0; it < 2; ++it) {
-                    const int i = 32 * it + l32;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        T y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = (T)(o[it][4 * q + e] * sw.out_scale);
-                        u32x2 w;
-                        __builtin_memcpy(&w, y, 8);
-                        *reinterpret_cast<u32x2 *>(&s.o[wave][i][8 * (q ^ ((i >> 2) & 3)) + 4 * half]) = w;
-                    }
-                }
-                T *out = static_cast<T *>(sw.out) + row0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = 16 * k + lane / 4, q = lane & 3;
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(&s.o[wave][i][8 * (q ^ ((i >> 2) & 3))]);
-                    if (i < cnt && wave * 32 + 8 * q < n) {
-                        T *to = out + i * step + 8 * q;
-                        if (sw.out_aligned) {
-                            *reinterpret_cast<u32x4 *>(to) = w;
-                        } else {
-                            uint16_t *h = reinterpret_cast<uint16_t *>(to);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (wave * 32 + 8 * q + e < n)
-                                    h[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-                        }
-                    }
-                }
+                for (int it = 0; it < IT; ++it)
+                    o[it] *= by;
+                if (sizeof(T) == 4 || sw.out_f32)
+                    put_out<float, IT>(o, static_cast<float *>(sw.out) + row0, step, cnt, wave * 16, n,
+                                       sw.out_aligned);
+                else
+                    put_out<T, IT>(o, static_cast<T *>(sw.out) + row0, step, cnt, wave * 16, n,
+                                   sw.out_aligned);
             }
         }
+
+        // The state past the chunk.
+        if (active) {
+            // The state is decayed by floats whose product follows p^(tokens)
+            // itself: the rounding of one is made up for by the next.
+            const double exact = whole * drift;
+            float decay = (float)exact;
+            drift = decay > 0.f && decay < __builtin_inff()
+                        ? 1.0 + (exact - (double)decay) * (double)__builtin_amdgcn_rcpf(decay)
+                        : 1.0;
+            drift = uniform_double(drift);
+            float by = 1.f;
+            if constexpr (F16) {
+                int to = 29 - ec - above_exponent(wt_max);
+                to = to < -60 ? -60 : to > 60 ? 60 : to;
+                bound = uniform_float(bound * decay + wt_sum * power2(eb + ec - 28));
+                decay *= power2(to - sigma);
+                sigma = to;
+                by = power2(sigma);
+            }
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        z[kk][u][r] *= decay;
+#pragma unroll 1
+            for (int ks = 0; ks < KS; ++ks) {
+                u32x4 cf[IP];
+#pragma unroll
+                for (int p = 0; p < IP; ++p)
+                    cf[p] = column_frag<S::LD>(ccol + (p * C + 32 * ks) * S::LD);
+                float x[8];
+                const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&s.wt[32 * ks + 4 * g4]);
+                const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&s.wt[32 * ks + 16 + 4 * g4]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = value16<F16>(cf[0][e / 2], e & 1);
+#pragma unroll
+                    for (int p = 1; p < IP; ++p)
+                        x[e] += value16<F16>(cf[p][e / 2], e & 1);
+                    x[e] *= e < 4 ? w0[e] : w1[e - 4];
+                    if constexpr (F16)
+                        x[e] *= by;
+                }
+                u32x4 xf[WP];
+                if (bad)
+                    parts_of<WP, F16, false>(x, xf);
+                else
+                    parts_of<WP, F16, true>(x, xf);
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int v = 0; v < IP; ++v) {
+                            const u32x4 bf =
+                                column_frag<S::LD>(bcol + (v * C + 32 * ks) * S::LD + 32 * kk + 16 * u);
+#pragma unroll
+                            for (int p = 0; p + v < WP; ++p)
+                                z[kk][u] = mma<F16>(bf, xf[p], z[kk][u]);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if constexpr (F16 && !STATES)
+                if (bad)
+                    find_bound();
+        }
+
         at = next;
         cnt = next_cnt;
     }
 
+    if (!active)
+        return;
+    if constexpr (F16) {
+        const float by = power2(-sigma);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                z[kk][u] *= by;
+    }
     if (STATES) {
+        float *seg = seg_of(blockIdx.x);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                seg[(mt * 16 + r) * 64] = z[mt][r];
+            for (int u = 0; u < 2; ++u)
+                *reinterpret_cast<f32x4 *>(seg + kk * 512 + 4 * u) = z[kk][u];
     } else if (sw.state_out && pl.last && col < n) {
         float *st = sw.state_out + sh * ((uint64_t)m * n) + col * sw.state_n;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = mt * 32 + 16 * (r / 8) + 8 * half + r % 8;
+            for (int e = 0; e < 8; ++e) {
+                const int row = kk * 32 + e / 4 * 16 + 4 * g4 + e % 4;
                 if (row < m)
-                    st[row * sw.state_m] = z[mt][r];
+                    st[row * sw.state_m] = z[kk][e / 4][e % 4];
             }
     }
 }
@@ -571,42 +830,53 @@ void run_split(const SweepSet &set, hipStream_t stream)
 {
     const dim3 grid(set.items, set.heads, (unsigned)set.count);
     if (set.seg_len) {
-        sweep_split_kernel<T, D, VEC, WP, true><<<grid, D * 2, 0, stream>>>(set);
-        launch_segment_scan(set, D, stream);
+        sweep_split_kernel<T, D, VEC, WP, true><<<grid, D * 4, 0, stream>>>(set);
+        if (set.tokens > kFewSegments * set.seg_len)
+            launch_segment_scan(set, D, stream);
     }
-    sweep_split_kernel<T, D, VEC, WP, false><<<grid, D * 2, 0, stream>>>(set);
+    sweep_split_kernel<T, D, VEC, WP, false><<<grid, D * 4, 0, stream>>>(set);
 }
 
-template <class T, int D>
+// Parts of the decayed rows: see "How exact".
+template <class T, int D, bool VEC>
 void split_of(const SweepSet &set, hipStream_t stream)
 {
-    bool states = false;
-    for (int i = 0; i < set.count; ++i)
-        states |= set.s[i].state_out != nullptr;
-    if (set.aligned && states)
-        run_split<T, D, true, 3>(set, stream);
+    if constexpr (sizeof(T) == 4) {
+        run_split<T, D, VEC, 3>(set, stream);
+    } else if constexpr (In<T>::kScaled) {
+        run_split<T, D, VEC, 2>(set, stream);
+    } else {
+        bool states = false;
+        for (int i = 0; i < set.count; ++i)
+            states |= set.s[i].state_out != nullptr;
+        if (states)
+            run_split<T, D, VEC, 3>(set, stream);
+        else
+            run_split<T, D, VEC, 2>(set, stream);
+    }
+}
+
+template <class T>
+void split_by_width(const SweepSet &set, int width, hipStream_t stream)
+{
+    if (width == 64 && set.aligned)
+        split_of<T, 64, true>(set, stream);
+    else if (width == 64)
+        split_of<T, 64, false>(set, stream);
     else if (set.aligned)
-        run_split<T, D, true, 2>(set, stream);
-    else if (states)
-        run_split<T, D, false, 3>(set, stream);
+        split_of<T, 128, true>(set, stream);
     else
-        run_split<T, D, false, 2>(set, stream);
+        split_of<T, 128, false>(set, stream);
 }
 
 }  // namespace
 
 void launch_sweeps_split(const SweepSet &set, int width, hipStream_t stream)
 {
-    if (set.dtype == LIBSCAN_BF16) {
-        if (width <= 64)
-            split_of<__bf16, 64>(set, stream);
-        else
-            split_of<__bf16, 128>(set, stream);
-    } else {
-        if (width <= 64)
-            split_of<_Float16, 64>(set, stream);
-        else
-            split_of<_Float16, 128>(set, stream);
+    switch (set.dtype) {
+    case LIBSCAN_F32: return split_by_width<float>(set, width, stream);
+    case LIBSCAN_BF16: return split_by_width<__bf16>(set, width, stream);
+    default: return split_by_width<_Float16>(set, width, stream);
     }
 }
 
