@@ -298,7 +298,14 @@ bool rows_aligned(const linattn_shape_t &s, const Rows &r, uint32_t width)
 {
     const size_t b = element_bytes(s.dtype);
     return (uintptr_t)r.p % 16 == 0 && width * b % 16 == 0 && r.seq * (int64_t)b % 16 == 0 &&
-           r.tok * (int64_t)b % 16 == 0 && r.head * (int64_t)b % 16 == 0;
+           r.tok * (int64_t)b % 16 == 0 && r.head * (int64_t)b % 16 == 0 &&
+           // a chunk of 64 within 32 bits
+           r.tok >= 0 && (uint64_t)r.tok * b < ((uint64_t)1 << 25);
+}
+
+int widest(const linattn_shape_t &s)
+{
+    return (int)(s.key_width > s.value_width ? s.key_width : s.value_width);
 }
 
 // Everything of a set but its sweeps.
@@ -312,7 +319,7 @@ SweepSet sweep_set(const linattn_shape_t &s, int count)
     set.seqs = s.seqs;
     set.heads = s.heads;
     set.tokens = s.tokens;
-    set.seg_len = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count);
+    set.seg_len = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count, widest(s));
     set.items = (uint32_t)linattn_items(s.tokens, s.ends != nullptr, s.seqs, set.seg_len);
     return set;
 }
@@ -322,14 +329,13 @@ size_t segment_bytes(const linattn_shape_t &s, int count)
     const SweepSet set = sweep_set(s, count);
     if (!set.seg_len)
         return 0;
-    const int width = (int)(s.key_width > s.value_width ? s.key_width : s.value_width);
-    return round_up((size_t)count * set.items * s.heads * linattn_state_floats(width) * sizeof(float),
+    return round_up((size_t)count * set.items * s.heads * linattn_state_floats(widest(s)) * sizeof(float),
                     kScratchAlign);
 }
 
 bool too_many_items(const linattn_shape_t &s, int count)
 {
-    const uint64_t l = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count);
+    const uint64_t l = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count, widest(s));
     return linattn_items(s.tokens, s.ends != nullptr, s.seqs, l) > (1u << 26);
 }
 
@@ -350,7 +356,7 @@ void out_of(const linattn_shape_t &s, Sweep &w, const linattn_rows_t &r, float *
     w.out_head = w.out_f32 ? (int64_t)width : r.head_stride;
     w.out_tok = w.out_f32 ? (int64_t)s.heads * width : r.token_stride;
     w.out_seq = s.ends ? 0 : (w.out_f32 ? (int64_t)s.tokens * s.heads * width : r.seq_stride);
-    w.out_aligned = w.out_f32 ? width % 4 == 0 : rows_aligned(s, rows_of(s, r), width);
+    w.out_aligned = w.out_f32 ? width % 4 == 0 && w.out_tok < (1 << 23) : rows_aligned(s, rows_of(s, r), width);
 }
 
 }  // namespace

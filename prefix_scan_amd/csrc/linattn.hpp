@@ -74,7 +74,8 @@ struct SweepSet {
 
 // Tokens per segment for a set of sweeps (0: no cutting) and the number of
 // (sequence, segment) items a grid has to cover.
-uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps);
+uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps,
+                         int width);
 uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len);
 // Floats of segment states one item of one head of one sweep takes.
 size_t linattn_state_floats(int width);

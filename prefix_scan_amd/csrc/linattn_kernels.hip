@@ -181,16 +181,32 @@ void run_step(const StepArgs &a, hipStream_t stream)
 
 size_t linattn_state_floats(int width) { return width <= 64 ? 64 * 64 : 128 * 128; }
 
-uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps)
+uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps,
+                         int width)
 {
-    // Equal shares of the tokens for 1024 workgroups, in whole chunks, but
-    // not so short that the states outweigh the rows.
-    const uint64_t rows = ragged ? tokens : tokens * seqs;
-    uint64_t share = (rows * heads * (uint64_t)sweeps + 1023) / 1024;
-    share = (share + 63) / 64 * 64;
-    if (share < 256)
-        share = 256;
-    return tokens > share ? share : 0;
+    // One workgroup for every place on the GPU, and no more: two of 128
+    // columns a compute unit, four of 64.  4 x 32 sequences and heads of 4096
+    // tokens take 239, 202, 236 and 242 us in 2, 4, 6 and 8 segments each
+    // (256, 512, 768 and 1024 workgroups); 16 heads of 65537 take 679, 456,
+    // 529 and 552 us in segments of 4096, 2048, 1408 and 1024.  Segments of
+    // under 256 tokens would move more of states than of rows.
+    const uint64_t places = width <= 64 ? 1024 : 512, lines = (uint64_t)heads * sweeps;
+    if (ragged) {
+        uint64_t share = (tokens * lines + places - 1) / places;
+        // Enough sequences as they are: only what is far longer than its
+        // share is cut (37 of 480 tokens each on average, 24 heads: 222 us
+        // whole, 262 us in shares).
+        if (seqs * lines >= places)
+            share *= 3;
+        share = (share + 63) / 64 * 64;
+        if (share < 256)
+            share = 256;
+        return tokens > share ? share : 0;
+    }
+    uint64_t segs = places / (lines * seqs);
+    if (segs > tokens / 256)
+        segs = tokens / 256;
+    return segs > 1 ? ((tokens + segs - 1) / segs + 63) / 64 * 64 : 0;
 }
 
 uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len)

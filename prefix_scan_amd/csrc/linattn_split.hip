@@ -48,6 +48,8 @@
 
 #include "../../include/libscan.h"
 
+#include <type_traits>
+
 namespace libscan {
 
 namespace {
@@ -194,33 +196,61 @@ struct Unit {
     u32x4 w[sizeof(T) / 2];
 };
 
-// This thread's units of rows [0, cnt) of a chunk, zeros past them.
+// A tensor's rows of one sequence and head.
+template <class T>
+struct Lines {
+    const T *p;                  // of the sequence's first token
+    int64_t tok;
+    __device__ __forceinline__ Lines(const Rows &r, uint64_t seq, uint64_t first, uint32_t head)
+        : p(row_ptr<T>(r, seq, first, head)), tok(r.tok)
+    {
+    }
+};
+
+// This thread's units of the rows of cnt tokens from the one at `at` on, back
+// where REV; zeros past them.  A whole chunk's addresses are a scalar and a
+// lane's 32 bits (the host sees to it that those hold them).
 template <class T, bool VEC, int W, int THREADS, int N>
-__device__ __forceinline__ void fetch(Unit<T> (&r)[N], const T *base, int64_t step, int cnt, int width)
+__device__ __forceinline__ void fetch(Unit<T> (&r)[N], const Lines<T> &from, uint64_t at, bool rev, int cnt,
+                                      int width)
 {
-    constexpr int PER = W / 8, RS = THREADS / PER;
-    static_assert(N == In<T>::kChunk / RS, "a chunk of rows");
-    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, col = tid % PER * 8;
-    const T *p = base + row0 * step + col;
-    if (VEC && cnt == In<T>::kChunk && width == W) {
+    constexpr int PER = W / 8, RS = THREADS / PER, H = (int)sizeof(T) / 2, C = In<T>::kChunk;
+    static_assert(N == C / RS, "a chunk of rows");
+    if (VEC && cnt == C) {
+        const char *base = reinterpret_cast<const char *>(from.p + (int64_t)(rev ? at - (C - 1) : at) * from.tok);
+        const int64_t step = (rev ? -RS : RS) * from.tok * (int64_t)sizeof(T);
+        const uint32_t tid = afresh((int)threadIdx.x), row = tid / PER, col = tid % PER * 8;
+        const uint32_t place = ((rev ? C - 1 - row : row) * (uint32_t)from.tok + col) * (uint32_t)sizeof(T);
+        if (width == W) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
+            for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-                r[k].w[h] = reinterpret_cast<const u32x4 *>(p)[h];
-            p += RS * step;
+                for (int h = 0; h < H; ++h)
+                    r[k].w[h] = *reinterpret_cast<const u32x4 *>(base + k * step + place + 16 * h);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    r[k].w[h] = u32x4{0, 0, 0, 0};
+                    if ((int)col + 4 * h < width)
+                        r[k].w[h] = *reinterpret_cast<const u32x4 *>(base + k * step + place + 16 * h);
+                }
         }
         return;
     }
+    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, col = tid % PER * 8;
+    const int64_t step = rev ? -from.tok : from.tok;
+    const T *p = from.p + (int64_t)at * from.tok + row0 * step + col;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
 #pragma unroll
-        for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+        for (int h = 0; h < H; ++h)
             r[k].w[h] = u32x4{0, 0, 0, 0};
         if (row0 + k * RS < cnt && col < width) {
             if (VEC) {
 #pragma unroll
-                for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                for (int h = 0; h < H; ++h)
                     if (h == 0 || col + 4 < width)
                         r[k].w[h] = reinterpret_cast<const u32x4 *>(p)[h];
             } else if constexpr (sizeof(T) == 4) {
@@ -363,35 +393,97 @@ __device__ __forceinline__ int above_exponent(float x) { return (int)(__float_as
 
 // This lane's row and four of the 16 columns from `first` of each tile.
 template <class T, int IT>
-__device__ __forceinline__ void put_out(const f32x4 *o, T *out, int64_t step, int cnt, int first, int n,
-                                        bool aligned)
+__device__ __forceinline__ void put_out(const f32x4 *o, T *out, int64_t tok, uint64_t at, bool rev, int cnt,
+                                        int first, int n, bool aligned)
 {
     typedef T t4 __attribute__((ext_vector_type(4)));
-    const int lane = afresh((int)threadIdx.x & 63), row = lane & 15, c0 = first + lane / 16 * 4;
+    const int lane = afresh((int)threadIdx.x & 63), c0 = lane / 16 * 4, row = lane & 15;
+    out += first;
     if (aligned && cnt == 16 * IT) {
-        T *to = out + row * step + c0;
-        if (c0 < n) {
+        char *base = reinterpret_cast<char *>(out + (int64_t)(rev ? at - (16 * IT - 1) : at) * tok);
+        const int64_t step = (rev ? -16 : 16) * tok * (int64_t)sizeof(T);
+        const uint32_t place = (uint32_t)(rev ? 16 * IT - 1 - row : row) * (uint32_t)tok + c0;
+        if (first + c0 < n) {
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                *reinterpret_cast<t4 *>(to) = __builtin_convertvector(o[it], t4);
-                to += 16 * step;
-            }
+            for (int it = 0; it < IT; ++it)
+                *reinterpret_cast<t4 *>(base + it * step + place * (uint32_t)sizeof(T)) =
+                    __builtin_convertvector(o[it], t4);
         }
         return;
     }
-    T *to = out + row * step + c0;
+    const int64_t step = rev ? -tok : tok;
+    T *to = out + (int64_t)at * tok + row * step + c0;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (16 * it + row < cnt && c0 + e < n)
+            if (16 * it + row < cnt && first + c0 + e < n)
                 to[e] = (T)o[it][e];
         to += 16 * step;
     }
 }
 
+// A chunk's outputs in LDS, whole rows in pieces of 16 bytes that trade places
+// by row, so that neither columns nor rows meet a bank twice.
+template <class T, int D>
+struct OutRows {
+    static constexpr int V = 16 / (int)sizeof(T), PIECES = D / V;
+    T x[In<T>::kChunk][D];
+    __device__ __forceinline__ T *at(int row, int piece) { return &x[row][(piece ^ (row & (PIECES - 1))) * V]; }
+};
+
+template <class T, int D, int IT>
+__device__ __forceinline__ void hold_rows(OutRows<T, D> &s, const f32x4 *o, int wave, int l16, int g4)
+{
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    constexpr int V = 16 / (int)sizeof(T);
+    const int c0 = wave * 16 + 4 * g4;
+#pragma unroll
+    for (int it = 0; it < IT; ++it)
+        *reinterpret_cast<t4 *>(s.at(16 * it + l16, c0 / V) + c0 % V) = __builtin_convertvector(o[it], t4);
+}
+
+// From there to memory, 16 bytes a lane.
+template <class T, int D, int THREADS>
+__device__ __forceinline__ void put_rows(OutRows<T, D> &s, T *out, int64_t tok, uint64_t at, bool rev, int cnt,
+                                         int n, bool aligned)
+{
+    constexpr int C = In<T>::kChunk, V = OutRows<T, D>::V, PER = OutRows<T, D>::PIECES, RS = THREADS / PER;
+    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, piece = tid % PER, col = piece * V;
+    if (aligned && cnt == C) {
+        char *base = reinterpret_cast<char *>(out + (int64_t)(rev ? at - (C - 1) : at) * tok);
+        const int64_t step = (rev ? -RS : RS) * tok * (int64_t)sizeof(T);
+        const uint32_t place =
+            ((uint32_t)(rev ? C - 1 - row0 : row0) * (uint32_t)tok + (uint32_t)col) * (uint32_t)sizeof(T);
+        if (col < n) {
+#pragma unroll
+            for (int k = 0; k < C / RS; ++k)
+                *reinterpret_cast<u32x4 *>(base + k * step + place) =
+                    *reinterpret_cast<const u32x4 *>(s.at(row0 + k * RS, piece));
+        }
+        return;
+    }
+    const int64_t step = rev ? -tok : tok;
+    T *to = out + (int64_t)at * tok + row0 * step + col;
+#pragma unroll
+    for (int k = 0; k < C / RS; ++k) {
+        const T *x = s.at(row0 + k * RS, piece);
+        if (row0 + k * RS < cnt) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (col + e < n)
+                    to[e] = x[e];
+        }
+        to += RS * step;
+    }
+}
+
+// VIA: outputs go through LDS, and out with the next chunk's loads; f16 rows
+// of 128 leave no room for that beside a second workgroup.
 template <class T, int D, bool STATES>
 struct Lds {
+    static constexpr bool VIA = !STATES && !(In<T>::kScaled && D == 128);
+    struct None {};
     static constexpr int C = In<T>::kChunk, IP = In<T>::kParts, OP = In<T>::kMade;
     static constexpr int LA = D + 8, LD = D + 16, LP = C + 8;
     uint16_t a[STATES ? 1 : IP][STATES ? 1 : C][LA];
@@ -399,10 +491,11 @@ struct Lds {
     uint16_t c[IP][C][LD];
     uint16_t p[STATES ? 1 : OP][STATES ? 1 : C][LP];
     float pw[C + 4], pl[C + 4];            // powers of the decay: hi, lo
-    float pair[C + 16];                    // pair_scale p^d at 16 + d, 0 for d < 0
+    float pair[C + 16];                    // pair_scale out_scale p^d at 16 + d, 0 for d < 0
     float wt[C];                           // pair_scale p^(cnt-1+shift-j)
     int bad[2];
     int exponent[2][4];                    // of a, b, c
+    alignas(16) typename std::conditional<VIA, OutRows<T, D>, None>::type o;
 };
 
 // STATES: only the segment's own contribution to the state, into set.seg.
@@ -417,10 +510,27 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     typedef Lds<T, D, STATES> S;
     __shared__ __align__(16) S s;
 
-    const Sweep &sw = set.s[blockIdx.z];
-    const uint32_t head = blockIdx.y;
+    // Of a gradient's three sweeps over the same rows, two read the same ones
+    // at the same time: they follow each other on one of the 8 dies (blocks
+    // go round them), so that its cache has the rows for all.
+    uint32_t sweep = 0, item = blockIdx.x, head = blockIdx.y;
+    if (set.count > 1) {
+        const uint64_t units = (uint64_t)set.items * set.heads, n = units / 8 * 8 * set.count;
+        const uint64_t b = item + set.items * (head + (uint64_t)set.heads * blockIdx.z);
+        uint64_t unit;
+        if (b < n) {
+            sweep = (uint32_t)(b / 8 % set.count);
+            unit = b / 8 / set.count * 8 + b % 8;
+        } else {
+            sweep = (uint32_t)((b - n) % set.count);
+            unit = units / 8 * 8 + (b - n) / set.count;
+        }
+        item = (uint32_t)(unit % set.items);
+        head = (uint32_t)(unit / set.items);
+    }
+    const Sweep &sw = set.s[sweep];
     Place pl;
-    if (!place_of(set, blockIdx.x, &pl))
+    if (!place_of(set, item, &pl))
         return;
     pl.seq = uniform(pl.seq);
     pl.first = uniform64(pl.first);
@@ -438,7 +548,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         const int d = i - 16;
         const Power p = d >= 0 ? decay_power(g, (double)d) : Power{0.f, 0.f};
         if (d < C)
-            s.pair[i] = sw.pair_scale * p.hi;
+            s.pair[i] = sw.pair_scale * sw.out_scale * p.hi;
         if (d >= 0) {
             s.pw[d] = p.hi;
             s.pl[d] = p.lo;
@@ -463,8 +573,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             z[kk][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto seg_of = [&](uint32_t item) {
-        return set.seg + (((uint64_t)blockIdx.z * set.items + item) * set.heads + head) * (D * D) +
+    const auto seg_of = [&](uint32_t at) {
+        return set.seg + (((uint64_t)sweep * set.items + at) * set.heads + head) * (D * D) +
                (wave * KK * 64 + lane) * 8;
     };
     if (!STATES && active) {
@@ -474,7 +584,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             const uint32_t before = few ? (uint32_t)(pl.lo / set.seg_len) : 1;
             const Power w = decay_power(g, (double)set.seg_len);
             for (uint32_t k = 0; k < before; ++k) {
-                const float *seg = seg_of(few ? blockIdx.x - before + k : blockIdx.x);
+                const float *seg = seg_of(few ? item - before + k : item);
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -516,16 +626,27 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     if constexpr (F16 && !STATES)
         find_bound();
 
-    const int64_t dir = sw.rev ? -1 : 1;
-    const T *pa = row_ptr<T>(sw.a, pl.seq, 0, head), *pb = row_ptr<T>(sw.b, pl.seq, 0, head),
-            *pc = row_ptr<T>(sw.c, pl.seq, 0, head);
+    const bool rev = sw.rev;
+    const Lines<T> la(sw.a, pl.seq, pl.first, head), lb(sw.b, pl.seq, pl.first, head),
+        lc(sw.c, pl.seq, pl.first, head);
+    const int64_t out0 = (int64_t)pl.seq * sw.out_seq + (int64_t)pl.first * sw.out_tok +
+                         (int64_t)head * sw.out_head;
+    int held_cnt = 0;            // outputs in s.o, and their first token
+    uint64_t held_at = 0;
+    const auto put_held = [&]() {
+        if constexpr (S::VIA)
+            if (held_cnt)
+                put_rows<T, D, THREADS>(s.o, static_cast<T *>(sw.out) + out0, sw.out_tok, held_at, rev,
+                                        held_cnt, n, sw.out_aligned);
+        held_cnt = 0;
+    };
     Unit<T> ra[STATES ? 1 : N], rb[N], rc[N];
     const auto fetch_chunk = [&](uint64_t at, int cnt) {
-        const int64_t tok = (int64_t)(pl.first + (sw.rev ? pl.len - 1 - at : at));
+        const uint64_t tok = rev ? pl.len - 1 - at : at;
         if constexpr (!STATES)
-            fetch<T, VEC, D, THREADS>(ra, pa + tok * sw.a.tok, dir * sw.a.tok, cnt, m);
-        fetch<T, VEC, D, THREADS>(rb, pb + tok * sw.b.tok, dir * sw.b.tok, cnt, m);
-        fetch<T, VEC, D, THREADS>(rc, pc + tok * sw.c.tok, dir * sw.c.tok, cnt, n);
+            fetch<T, VEC, D, THREADS>(ra, la, tok, rev, cnt, m);
+        fetch<T, VEC, D, THREADS>(rb, lb, tok, rev, cnt, m);
+        fetch<T, VEC, D, THREADS>(rc, lc, tok, rev, cnt, n);
     };
     // This lane's places: along the rows of a, b and the scores, and down the
     // columns of b and c.
@@ -593,6 +714,9 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         const uint64_t next = at + cnt;
         const uint64_t left = pl.hi - next;
         const int next_cnt = left == 0 ? 0 : next < single ? 1 : (int)(left < C ? left : C);
+        // The outputs of the chunk before go out ahead of these loads, which are
+        // waited for in order.
+        put_held();
         if (next_cnt)
             fetch_chunk(next, next_cnt);
 
@@ -649,7 +773,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 #pragma unroll
             for (int it = 0; it < IT; ++it)
                 o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (active) {
+            {
                 const float by = F16 ? power2(tau - sigma) : 1.f;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
@@ -672,7 +796,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 }
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    float w = s.pw[16 * it + oi + 1 - sw.shift];
+                    float w = s.pw[16 * it + oi + 1 - sw.shift] * sw.out_scale;
                     if constexpr (F16)
                         w = w * power2(rho - tau);
 #pragma unroll
@@ -685,7 +809,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 
         // What they read of the chunk's own tokens.
         if constexpr (!STATES) {
-            if (active) {
+            {
                 const int own = afresh(lane);
                 lds_u16 *const prow = (lds_u16 *)&s.p[0][0][0] + (own & 15) * S::LP + own / 16 * 8;
 #pragma unroll
@@ -704,25 +828,27 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                                 o[it] = mma<F16>(cf[u], pf, o[it]);
                         }
                 }
-                const uint64_t t0 = pl.first + (sw.rev ? pl.len - 1 - at : at);
-                const int64_t step = dir * sw.out_tok;
-                const int64_t row0 = (int64_t)pl.seq * sw.out_seq + (int64_t)t0 * sw.out_tok +
-                                     (int64_t)head * sw.out_head;
-                const float by = F16 ? sw.out_scale * power2(-rho) : sw.out_scale;
+                if constexpr (F16) {
+                    const float by = power2(-rho);
 #pragma unroll
-                for (int it = 0; it < IT; ++it)
-                    o[it] *= by;
-                if (sizeof(T) == 4 || sw.out_f32)
-                    put_out<float, IT>(o, static_cast<float *>(sw.out) + row0, step, cnt, wave * 16, n,
-                                       sw.out_aligned);
-                else
-                    put_out<T, IT>(o, static_cast<T *>(sw.out) + row0, step, cnt, wave * 16, n,
-                                   sw.out_aligned);
+                    for (int it = 0; it < IT; ++it)
+                        o[it] *= by;
+                }
+                held_at = rev ? pl.len - 1 - at : at;
+                if (sizeof(T) == 2 && sw.out_f32) {
+                    put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, held_at, rev, cnt,
+                                       wave * 16, n, sw.out_aligned);
+                } else if constexpr (S::VIA) {
+                    hold_rows<T, D, IT>(s.o, o, wave, l16, g4);
+                    held_cnt = cnt;
+                } else {
+                    put_out<T, IT>(o, static_cast<T *>(sw.out) + out0, sw.out_tok, held_at, rev, cnt,
+                                   wave * 16, n, sw.out_aligned);
+                }
             }
         }
-
         // The state past the chunk.
-        if (active) {
+        {
             // The state is decayed by floats whose product follows p^(tokens)
             // itself: the rounding of one is made up for by the next.
             const double exact = whole * drift;
@@ -795,6 +921,9 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         cnt = next_cnt;
     }
 
+    if constexpr (S::VIA)
+        __syncthreads();
+    put_held();
     if (!active)
         return;
     if constexpr (F16) {
@@ -806,7 +935,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 z[kk][u] *= by;
     }
     if (STATES) {
-        float *seg = seg_of(blockIdx.x);
+        float *seg = seg_of(item);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
