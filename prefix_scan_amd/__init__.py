@@ -226,6 +226,19 @@ _outgrown = []          # kept: a captured graph may hold their addresses
 _scratch_lock = threading.Lock()
 
 
+# The current stream's handle, by the short way where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _scratch_at(device, index, handle, stream, nbytes):
+    """_scratch_for, by the stream's handle: a buffer that is large enough is found at once."""
+    buf = _scratch.get((index, handle))
+    if buf is None or buf.numel() < nbytes:
+        buf = _scratch_for(device, stream or torch.cuda.current_stream(device), nbytes)
+    return buf
+
+
 def _scratch_for(device, stream_obj, nbytes):
     key = (device.index, stream_obj.cuda_stream)
     with _scratch_lock:
@@ -618,13 +631,47 @@ def _dev_dense(t, name, dtype, shape, device):
     return t
 
 
+# What the checks of a call's tensors found, by the tensors' layouts: shapes,
+# strides, types and devices, never addresses or values.
+_plans = {}
+
+
+def _layout(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _planned(make, *tensors):
+    try:
+        key = (make, *map(_layout, tensors))
+    except AttributeError:              # something is no tensor: the checks say which
+        return make(*tensors)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = make(*tensors)
+        if len(_plans) >= 1024:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
 def _rows(t, packed):
-    """A [B, T, H, D] tensor's rows, a packed [N, H, D] one's or a step's [B, H, D]."""
+    """(strides of sequence, token and head, heads) of a [B, T, H, D] tensor's rows, a packed
+    [N, H, D] one's or a step's [B, H, D]."""
     seq, tok = (0, t.stride(0)) if packed else (t.stride(0), t.stride(1) if t.dim() == 4 else 0)
-    return _Rows(t.data_ptr(), seq, tok, t.stride(-2), t.shape[-2])
+    return seq, tok, t.stride(-2), t.shape[-2]
 
 
-def _shape_of(q, k, v, log_decay, scale, ends, dims):
+def _dense_rows(shape, packed):
+    """_rows of a new tensor."""
+    heads, width = shape[-2:]
+    if packed:
+        return 0, heads * width, width, heads
+    return (heads * width * (shape[1] if len(shape) == 4 else 1),
+            heads * width if len(shape) == 4 else 0, width, heads)
+
+
+def _shape_of(q, k, v, log_decay, ends, dims):
+    """The call's _Shape without its pointers and scale."""
     _dev_rows(q, "q", dims=dims)
     device = q.device
     _dev_rows(k, "k", q.dtype, dims, device)
@@ -654,8 +701,7 @@ def _shape_of(q, k, v, log_decay, scale, ends, dims):
             raise ValueError("ends must be one number for each sequence, on %s" % device)
         seqs = ends.shape[0]
     return _Shape(_DTYPES[q.dtype], seqs, heads, q.shape[-1], v.shape[-1],
-                  q.shape[-3] if dims == 4 or ends is not None else 1,
-                  ends.data_ptr() if ends is not None else None, log_decay.data_ptr(), float(scale))
+                  q.shape[-3] if dims == 4 or ends is not None else 1)
 
 
 def _states(shape, t, name, device, count=None):
@@ -665,19 +711,65 @@ def _states(shape, t, name, device, count=None):
         device)
 
 
-def _new_states(shape, device):
-    return torch.empty((shape.seqs, shape.heads, shape.key_width, shape.value_width),
-                       dtype=torch.float32, device=device)
-
-
 def _out_like(out, name, want, dtype, device):
-    """`out`, checked, or a new tensor of that shape."""
-    if out is None:
-        return torch.empty(want, dtype=dtype, device=device)
-    _dev_rows(out, name, dtype, len(want), device)
-    if tuple(out.shape) != tuple(want):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(want), tuple(out.shape)))
+    """`out`, checked, or None."""
+    if out is not None:
+        _dev_rows(out, name, dtype, len(want), device)
+        if tuple(out.shape) != tuple(want):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(want), tuple(out.shape)))
     return out
+
+
+class _Plan:
+    """What a call's layout comes to: the _Shape's fields, and for each tensor of rows its
+    strides and the shape that a new one would have."""
+
+    def __init__(self, shape, q, rows, need):
+        self.fields = [getattr(shape, n) for n, _ in _Shape._fields_[:6]]
+        self.rows = rows
+        self.need = need
+        self.dtype, self.device, self.index = q.dtype, q.device, q.get_device()
+        self.states = (shape.seqs, shape.heads, shape.key_width, shape.value_width)
+
+    def shape(self, ends, log_decay, scale):
+        return _Shape(*self.fields, None if ends is None else ends.data_ptr(), log_decay.data_ptr(), scale)
+
+    def new(self, i):
+        return torch.empty(self.rows[i][1], dtype=self.dtype, device=self.device)
+
+    def new_states(self):
+        return torch.empty(self.states, dtype=torch.float32, device=self.device)
+
+    def stream(self, stream):
+        return _raw_stream(self.index) if stream is None else stream.cuda_stream
+
+    def scratch(self, handle, stream):
+        return _scratch_at(self.device, self.index, handle, stream, self.need)
+
+    def at(self, i, t):
+        return _Rows(t.data_ptr(), *self.rows[i][0])
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_plan(packed, *pairs):
+    """For each (tensor or None, its shape): (strides and heads, shape)."""
+    return [(_dense_rows(want, packed) if t is None else _rows(t, packed), tuple(want)) for t, want in pairs]
+
+
+def _linattn_plan(q, k, v, log_decay, ends, state, out, state_out):
+    packed = ends is not None
+    shape = _shape_of(q, k, v, log_decay, ends, 3 if packed else 4)
+    _states(shape, state, "state", q.device)
+    want = q.shape[:-2] + (shape.heads, shape.value_width)
+    _out_like(out, "out", want, q.dtype, q.device)
+    _states(shape, state_out, "state_out", q.device)
+    if packed:                          # no value of ends plays a part in the scratch's size
+        shape.ends = ends.data_ptr()
+    return _Plan(shape, q, _row_plan(packed, (q, q.shape), (k, k.shape), (v, v.shape), (out, want)),
+                 lib().linattn_scratch_bytes(shape))
 
 
 def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=False, out=None,
@@ -690,19 +782,34 @@ def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=Fal
     runs_layout_u32 leaves them) [N, H, D], the sequences one after another.
     state: float32 [B, H, Dk, Dv] before the first token (None: zeros).
     Returns (out, state_out), state_out None unless want_state or given."""
-    packed = ends is not None
-    shape = _shape_of(q, k, v, log_decay, scale, ends, 3 if packed else 4)
-    _states(shape, state, "state", q.device)
-    out = _out_like(out, "out", q.shape[:-2] + (shape.heads, shape.value_width), q.dtype, q.device)
+    p = _planned(_linattn_plan, q, k, v, log_decay, ends, state, out, state_out)
+    if out is None:
+        out = p.new(3)
     if state_out is None and want_state:
-        state_out = _new_states(shape, q.device)
-    _states(shape, state_out, "state_out", q.device)
-    sh, s = _stream_handle(q.device, stream)
-    scr = _scratch_for(q.device, s, lib().linattn_scratch_bytes(shape))
-    _check(lib().linattn(shape, _rows(q, packed), _rows(k, packed), _rows(v, packed), _ptr(state),
-                         _rows(out, packed), _ptr(state_out), _ptr(scr), scr.numel(), sh),
-           "linattn")
+        state_out = p.new_states()
+    handle = p.stream(stream)
+    scr = p.scratch(handle, stream)
+    _check(lib().linattn(p.shape(ends, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v), _addr(state),
+                         p.at(3, out), _addr(state_out), scr.data_ptr(), scr.numel(), handle), "linattn")
     return out, state_out
+
+
+def _linattn_grad_plan(dout, q, k, v, log_decay, ends, state, dstate_out, dq, dk, dv, dstate):
+    packed = ends is not None
+    shape = _shape_of(q, k, v, log_decay, ends, 3 if packed else 4)
+    _dev_rows(dout, "dout", q.dtype, q.dim(), q.device)
+    want = tuple(q.shape[:-2]) + (shape.heads, shape.value_width)
+    if tuple(dout.shape) != want:
+        raise ValueError("dout must have the shape of linattn's out, got %s" % (tuple(dout.shape),))
+    for t, name in ((state, "state"), (dstate_out, "dstate_out"), (dstate, "dstate")):
+        _states(shape, t, name, q.device)
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+        _out_like(t, name, like.shape, q.dtype, q.device)
+    if packed:
+        shape.ends = ends.data_ptr()
+    return _Plan(shape, q, _row_plan(packed, (dout, want), (q, q.shape), (k, k.shape), (v, v.shape),
+                                     (dq, q.shape), (dk, k.shape), (dv, v.shape)),
+                 lib().linattn_grad_scratch_bytes(shape, q.shape[-2], k.shape[-2], v.shape[-2]))
 
 
 def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dstate_out=None,
@@ -710,27 +817,35 @@ def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dst
     """The gradient of linattn: (dq, dk, dv, dstate) for out's gradient dout
     and state_out's dstate_out (None: zeros); dstate is None unless
     want_dstate or given.  Gradients of shared heads are summed."""
-    packed = ends is not None
-    shape = _shape_of(q, k, v, log_decay, scale, ends, 3 if packed else 4)
-    _dev_rows(dout, "dout", q.dtype, q.dim(), q.device)
-    if tuple(dout.shape) != tuple(q.shape[:-2]) + (shape.heads, shape.value_width):
-        raise ValueError("dout must have the shape of linattn's out, got %s" % (tuple(dout.shape),))
-    _states(shape, state, "state", q.device)
-    _states(shape, dstate_out, "dstate_out", q.device)
-    dq = _out_like(dq, "dq", q.shape, q.dtype, q.device)
-    dk = _out_like(dk, "dk", k.shape, q.dtype, q.device)
-    dv = _out_like(dv, "dv", v.shape, q.dtype, q.device)
+    p = _planned(_linattn_grad_plan, dout, q, k, v, log_decay, ends, state, dstate_out, dq, dk, dv, dstate)
+    dq, dk, dv = (p.new(i) if t is None else t for i, t in ((4, dq), (5, dk), (6, dv)))
     if dstate is None and want_dstate:
-        dstate = _new_states(shape, q.device)
-    _states(shape, dstate, "dstate", q.device)
-    sh, s = _stream_handle(q.device, stream)
-    scr = _scratch_for(q.device, s, lib().linattn_grad_scratch_bytes(
-        shape, q.shape[-2], k.shape[-2], v.shape[-2]))
-    _check(lib().linattn_grad(shape, _rows(dout, packed), _rows(q, packed), _rows(k, packed),
-                              _rows(v, packed), _ptr(state), _ptr(dstate_out), _rows(dq, packed),
-                              _rows(dk, packed), _rows(dv, packed), _ptr(dstate), _ptr(scr),
-                              scr.numel(), sh), "linattn_grad")
+        dstate = p.new_states()
+    handle = p.stream(stream)
+    scr = p.scratch(handle, stream)
+    _check(lib().linattn_grad(p.shape(ends, log_decay, scale), p.at(0, dout), p.at(1, q), p.at(2, k),
+                              p.at(3, v), _addr(state), _addr(dstate_out), p.at(4, dq), p.at(5, dk),
+                              p.at(6, dv), _addr(dstate), scr.data_ptr(), scr.numel(), handle),
+           "linattn_grad")
     return dq, dk, dv, dstate
+
+
+def _linattn_step_plan(q, k, v, log_decay, state, slots, out, state_out):
+    shape = _shape_of(q, k, v, log_decay, None, 3)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise TypeError("state must be a torch.Tensor of [P, H, Dk, Dv]")
+    pool = state.shape[0]
+    _states(shape, state, "state", q.device, pool)
+    _states(shape, state_out, "state_out", q.device, pool)
+    if slots is None:
+        if pool != shape.seqs:
+            raise ValueError("without slots, state must hold one state for each of %d rows, got %d"
+                             % (shape.seqs, pool))
+    else:
+        _dev_dense(slots, "slots", torch.int32, (shape.seqs,), q.device)
+    want = (shape.seqs, shape.heads, shape.value_width)
+    _out_like(out, "out", want, q.dtype, q.device)
+    return _Plan(shape, q, _row_plan(False, (q, q.shape), (k, k.shape), (v, v.shape), (out, want)), 0)
 
 
 def linattn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, state_out=None,
@@ -740,24 +855,32 @@ def linattn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, sta
     the float32 pool [P, H, Dk, Dv], in place or into state_out.  A row whose
     slot is outside the pool, as -1, gives zeros and touches nothing; no slot
     may be listed twice.  Returns (out, the pool that was written)."""
-    shape = _shape_of(q, k, v, log_decay, scale, None, 3)
-    if not isinstance(state, torch.Tensor) or state.dim() != 4:
-        raise TypeError("state must be a torch.Tensor of [P, H, Dk, Dv]")
-    pool = state.shape[0]
-    _states(shape, state, "state", q.device, pool)
-    state_out = state if state_out is None else _states(shape, state_out, "state_out", q.device, pool)
-    if slots is None:
-        if pool != shape.seqs:
-            raise ValueError("without slots, state must hold one state for each of %d rows, got %d"
-                             % (shape.seqs, pool))
-    else:
-        _dev_dense(slots, "slots", torch.int32, (shape.seqs,), q.device)
-    out = _out_like(out, "out", (shape.seqs, shape.heads, shape.value_width), q.dtype, q.device)
-    sh, _ = _stream_handle(q.device, stream)
-    _check(lib().linattn_step(shape, _rows(q, False), _rows(k, False), _rows(v, False), _ptr(state),
-                              pool, _ptr(slots), _rows(out, False), _ptr(state_out), sh),
-           "linattn_step")
+    if state_out is None:
+        state_out = state
+    p = _planned(_linattn_step_plan, q, k, v, log_decay, state, slots, out, state_out)
+    if out is None:
+        out = p.new(3)
+    _check(lib().linattn_step(p.shape(None, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v),
+                              state.data_ptr(), state.shape[0], _addr(slots), p.at(3, out),
+                              state_out.data_ptr(), p.stream(stream)), "linattn_step")
     return out, state_out
+
+
+def _sample_plan(logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, kept):
+    _dev_rows(logits, "logits", dims=2)
+    device, rows = logits.device, logits.shape[0]
+    if logits.shape[1] > SAMPLE_MAX_VOCAB:
+        raise ValueError("logits must have at most %d columns, got %d" % (
+            SAMPLE_MAX_VOCAB, logits.shape[1]))
+    _dev_dense(u, "u", torch.float32, (rows,), device)
+    for t, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
+                           (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32),
+                           (tokens, "tokens", torch.int32), (logprobs, "logprobs", torch.float32),
+                           (kept, "kept", torch.int32)):
+        if t is not None:
+            _dev_dense(t, name, dtype, (rows,), device)
+    return (_DTYPES[logits.dtype], rows, logits.shape[1], logits.stride(0), device, logits.get_device(),
+            lib().sample_scratch_bytes(rows, logits.shape[1]))
 
 
 def sample_logits(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None,
@@ -772,29 +895,23 @@ def sample_logits(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     index order, is passed.  temperature 0 is the largest logit.  Returns
     (tokens int32, logprobs float32, kept int32); a row with nothing but -inf
     and NaN gets token -1."""
-    _dev_rows(logits, "logits", dims=2)
-    device, rows = logits.device, logits.shape[0]
-    if logits.shape[1] > SAMPLE_MAX_VOCAB:
-        raise ValueError("logits must have at most %d columns, got %d" % (
-            SAMPLE_MAX_VOCAB, logits.shape[1]))
-    _dev_dense(u, "u", torch.float32, (rows,), device)
-    a = _Sample(_DTYPES[logits.dtype], rows, logits.shape[1], logits.data_ptr(), logits.stride(0),
-                u.data_ptr())
-    for value, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
-                               (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
-        if isinstance(value, torch.Tensor):
-            _dev_dense(value, name, dtype, (rows,), device)
-            setattr(a, name + "s", value.data_ptr())
-        else:
-            setattr(a, name, min(max(int(value), 0), 0x7FFFFFFF) if name == "top_k" else float(value))
-    outs = []
-    for t, name, dtype in ((tokens, "tokens", torch.int32), (logprobs, "logprobs", torch.float32),
-                           (kept, "kept", torch.int32)):
-        t = torch.empty(rows, dtype=dtype, device=device) if t is None else \
-            _dev_dense(t, name, dtype, (rows,), device)
-        setattr(a, name, t.data_ptr())
-        outs.append(t)
-    sh, s = _stream_handle(device, stream)
-    scr = _scratch_for(device, s, lib().sample_scratch_bytes(rows, logits.shape[1]))
-    _check(lib().sample_logits(a, _ptr(scr), scr.numel(), sh), "sample_logits")
-    return tuple(outs)
+    each = [t if isinstance(t, torch.Tensor) else None for t in (temperature, top_k, top_p, min_p)]
+    code, rows, vocab, stride, device, index, need = _planned(
+        _sample_plan, logits, u, *each, tokens, logprobs, kept)
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=device)
+    if logprobs is None:
+        logprobs = torch.empty(rows, dtype=torch.float32, device=device)
+    if kept is None:
+        kept = torch.empty(rows, dtype=torch.int32, device=device)
+    a = _Sample(code, rows, vocab, logits.data_ptr(), stride, u.data_ptr(),
+                1.0 if each[0] is not None else temperature,
+                1.0 if each[2] is not None else top_p,
+                0.0 if each[3] is not None else min_p,
+                0 if each[1] is not None else min(max(int(top_k), 0), 0x7FFFFFFF),
+                _addr(each[0]), _addr(each[2]), _addr(each[3]), _addr(each[1]),
+                tokens.data_ptr(), logprobs.data_ptr(), kept.data_ptr())
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    scr = _scratch_at(device, index, handle, stream, need)
+    _check(lib().sample_logits(a, scr.data_ptr(), scr.numel(), handle), "sample_logits")
+    return tokens, logprobs, kept

@@ -486,10 +486,10 @@ struct Lds {
     struct None {};
     static constexpr int C = In<T>::kChunk, IP = In<T>::kParts, OP = In<T>::kMade;
     static constexpr int LA = D + 8, LD = D + 16, LP = C + 8;
-    uint16_t a[STATES ? 1 : IP][STATES ? 1 : C][LA];
-    uint16_t b[IP][C][LD];
+    alignas(16) uint16_t a[STATES ? 1 : IP][STATES ? 1 : C][LA];
+    alignas(16) uint16_t b[IP][C][LD];
     uint16_t c[IP][C][LD];
-    uint16_t p[STATES ? 1 : OP][STATES ? 1 : C][LP];
+    alignas(16) uint16_t p[STATES ? 1 : OP][STATES ? 1 : C][LP];
     float pw[C + 4], pl[C + 4];            // powers of the decay: hi, lo
     float pair[C + 16];                    // pair_scale out_scale p^d at 16 + d, 0 for d < 0
     float wt[C];                           // pair_scale p^(cnt-1+shift-j)
@@ -544,6 +544,22 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     const int lane = threadIdx.x & 63, g4 = lane >> 4, l16 = lane & 15;
     const float g = set.log_decay[head];
     const int m = sw.m, n = sw.n;
+    const bool rev = sw.rev;
+    const Lines<T> la(sw.a, pl.seq, pl.first, head), lb(sw.b, pl.seq, pl.first, head),
+        lc(sw.c, pl.seq, pl.first, head);
+    Unit<T> ra[STATES ? 1 : N], rb[N], rc[N];
+    const auto fetch_chunk = [&](uint64_t at, int cnt) {
+        const uint64_t tok = rev ? pl.len - 1 - at : at;
+        if constexpr (!STATES)
+            fetch<T, VEC, D, THREADS>(ra, la, tok, rev, cnt, m);
+        fetch<T, VEC, D, THREADS>(rb, lb, tok, rev, cnt, m);
+        fetch<T, VEC, D, THREADS>(rc, lc, tok, rev, cnt, n);
+    };
+    uint64_t at = pl.lo, single = 0;   // tokens below `single` are taken one at a time
+    int cnt = pl.hi - at < C ? (int)(pl.hi - at) : C, cnt_wt = -1, turn = 0;
+    double whole = 1.0, drift = 1.0;   // p^cnt; what the factors so far left of it
+    float wt_max = 0.f, wt_sum = 0.f;
+    fetch_chunk(at, cnt);
     for (int i = threadIdx.x; i < C + 17; i += THREADS) {
         const int d = i - 16;
         const Power p = d >= 0 ? decay_power(g, (double)d) : Power{0.f, 0.f};
@@ -560,8 +576,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             s.exponent[threadIdx.x][i] = 0;
     }
     if constexpr (!STATES)                  // the scores' upper corner stays zero
-        for (int i = threadIdx.x; i < OP * C * S::LP; i += THREADS)
-            (&s.p[0][0][0])[i] = 0;
+        for (int i = threadIdx.x; i < OP * C * S::LP / 8; i += THREADS)
+            reinterpret_cast<u32x4 *>(&s.p[0][0][0])[i] = u32x4{0, 0, 0, 0};
 
     const int col = wave * 16 + l16;
     const bool active = wave * 16 < n;      // whether the wave has columns
@@ -626,9 +642,6 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     if constexpr (F16 && !STATES)
         find_bound();
 
-    const bool rev = sw.rev;
-    const Lines<T> la(sw.a, pl.seq, pl.first, head), lb(sw.b, pl.seq, pl.first, head),
-        lc(sw.c, pl.seq, pl.first, head);
     const int64_t out0 = (int64_t)pl.seq * sw.out_seq + (int64_t)pl.first * sw.out_tok +
                          (int64_t)head * sw.out_head;
     int held_cnt = 0;            // outputs in s.o, and their first token
@@ -640,25 +653,12 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                                         held_cnt, n, sw.out_aligned);
         held_cnt = 0;
     };
-    Unit<T> ra[STATES ? 1 : N], rb[N], rc[N];
-    const auto fetch_chunk = [&](uint64_t at, int cnt) {
-        const uint64_t tok = rev ? pl.len - 1 - at : at;
-        if constexpr (!STATES)
-            fetch<T, VEC, D, THREADS>(ra, la, tok, rev, cnt, m);
-        fetch<T, VEC, D, THREADS>(rb, lb, tok, rev, cnt, m);
-        fetch<T, VEC, D, THREADS>(rc, lc, tok, rev, cnt, n);
-    };
     // This lane's places: along the rows of a, b and the scores, and down the
     // columns of b and c.
     lds_u16 *const arow = (lds_u16 *)&s.a[0][0][0] + l16 * S::LA + 8 * g4;
     lds_u16 *const bcol = (lds_u16 *)&s.b[0][0][0] + (4 * g4 + l16 / 4) * S::LD + 4 * (l16 & 3);
     lds_u16 *const ccol = (lds_u16 *)&s.c[0][0][0] + (4 * g4 + l16 / 4) * S::LD + 4 * (l16 & 3) + wave * 16;
 
-    uint64_t at = pl.lo, single = 0;   // tokens below `single` are taken one at a time
-    int cnt = pl.hi - at < C ? (int)(pl.hi - at) : C, cnt_wt = -1, turn = 0;
-    double whole = 1.0, drift = 1.0;   // p^cnt; what the factors so far left of it
-    float wt_max = 0.f, wt_sum = 0.f;
-    fetch_chunk(at, cnt);
     while (at < pl.hi) {
         __syncthreads();
         if constexpr (!STATES)
