@@ -507,6 +507,9 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     constexpr int NW = D / 16, THREADS = D * 4, KK = D / 32, IT = C / 16, KS = C / 32;
     constexpr int N = C * D / 8 / THREADS;
     constexpr bool F16 = In<T>::kScaled;
+    // Whether columns and rows past the widths are left out.  bf16 rows have no
+    // registers for the branches.
+    constexpr bool SKIP = sizeof(T) == 4 || F16;
     typedef Lds<T, D, STATES> S;
     __shared__ __align__(16) S s;
 
@@ -739,6 +742,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
+                    if (SKIP && kk * 32 >= m)
+                        break;
                     u32x4 af[IP], bf[IP];
 #pragma unroll
                     for (int p = 0; p < IP; ++p) {
@@ -773,10 +778,12 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 #pragma unroll
             for (int it = 0; it < IT; ++it)
                 o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-            {
+            if (!SKIP || active) {
                 const float by = F16 ? power2(tau - sigma) : 1.f;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
+                    if (SKIP && kk * 32 >= m)
+                        break;
                     float x[8];
                     u32x4 zf[OP];
 #pragma unroll
@@ -809,7 +816,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 
         // What they read of the chunk's own tokens.
         if constexpr (!STATES) {
-            {
+            if (!SKIP || active) {
                 const int own = afresh(lane);
                 lds_u16 *const prow = (lds_u16 *)&s.p[0][0][0] + (own & 15) * S::LP + own / 16 * 8;
 #pragma unroll
@@ -834,21 +841,23 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     for (int it = 0; it < IT; ++it)
                         o[it] *= by;
                 }
-                held_at = rev ? pl.len - 1 - at : at;
-                if (sizeof(T) == 2 && sw.out_f32) {
-                    put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, held_at, rev, cnt,
+                const uint64_t tok = rev ? pl.len - 1 - at : at;
+                if (sizeof(T) == 2 && sw.out_f32)
+                    put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, tok, rev, cnt,
                                        wave * 16, n, sw.out_aligned);
-                } else if constexpr (S::VIA) {
+                else if constexpr (S::VIA)
                     hold_rows<T, D, IT>(s.o, o, wave, l16, g4);
-                    held_cnt = cnt;
-                } else {
-                    put_out<T, IT>(o, static_cast<T *>(sw.out) + out0, sw.out_tok, held_at, rev, cnt,
-                                   wave * 16, n, sw.out_aligned);
-                }
+                else
+                    put_out<T, IT>(o, static_cast<T *>(sw.out) + out0, sw.out_tok, tok, rev, cnt, wave * 16,
+                                   n, sw.out_aligned);
+            }
+            if (S::VIA && !(sizeof(T) == 2 && sw.out_f32)) {
+                held_at = rev ? pl.len - 1 - at : at;
+                held_cnt = cnt;
             }
         }
         // The state past the chunk.
-        {
+        if (!SKIP || active) {
             // The state is decayed by floats whose product follows p^(tokens)
             // itself: the rounding of one is made up for by the next.
             const double exact = whole * drift;
@@ -899,6 +908,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     parts_of<WP, F16, true>(x, xf);
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
+                    if (SKIP && kk * 32 >= m)
+                        break;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
