@@ -37,8 +37,9 @@
 // every 32: lane group g has 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3.  So
 // the accumulators of Z are the operand of Z^T A^T as they stand, and the
 // column reads of b and c go through 16 rows on end.  Rows of a and of the
-// scores are stored in that order and 8 elements longer than they need be,
-// those of b and c 16: no read meets a bank twice.
+// scores are stored in that order.  Rows of a, b and c are 16 elements longer
+// than they need be, those of the scores trade places by row: no read meets a
+// bank twice.
 //
 // The chunk is causal by selection, not by multiplication: a masked pair is
 // zero whatever the product was.  A value that is not finite would still
@@ -485,8 +486,9 @@ struct Lds {
     static constexpr bool VIA = !STATES && !(In<T>::kScaled && D == 128);
     struct None {};
     static constexpr int C = In<T>::kChunk, IP = In<T>::kParts, OP = In<T>::kMade;
-    static constexpr int LA = D + 8, LD = D + 16, LP = C + 8;
-    alignas(16) uint16_t a[STATES ? 1 : IP][STATES ? 1 : C][LA];
+    static constexpr int LD = D + 16, LP = C == 64 ? 64 : C + 16;
+    __device__ static constexpr int swap(int row) { return C == 64 ? (row >> 1 & 3) << 1 : 0; }
+    alignas(16) uint16_t a[STATES ? 1 : IP][STATES ? 1 : C][LD];
     alignas(16) uint16_t b[IP][C][LD];
     uint16_t c[IP][C][LD];
     alignas(16) uint16_t p[STATES ? 1 : OP][STATES ? 1 : C][LP];
@@ -658,7 +660,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     };
     // This lane's places: along the rows of a, b and the scores, and down the
     // columns of b and c.
-    lds_u16 *const arow = (lds_u16 *)&s.a[0][0][0] + l16 * S::LA + 8 * g4;
+    lds_u16 *const arow = (lds_u16 *)&s.a[0][0][0] + l16 * S::LD + 8 * g4;
     lds_u16 *const bcol = (lds_u16 *)&s.b[0][0][0] + (4 * g4 + l16 / 4) * S::LD + 4 * (l16 & 3);
     lds_u16 *const ccol = (lds_u16 *)&s.c[0][0][0] + (4 * g4 + l16 / 4) * S::LD + 4 * (l16 & 3) + wave * 16;
 
@@ -747,7 +749,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     u32x4 af[IP], bf[IP];
 #pragma unroll
                     for (int p = 0; p < IP; ++p) {
-                        af[p] = row_frag(arow + (p * C + 16 * it) * S::LA + 32 * kk);
+                        af[p] = row_frag(arow + (p * C + 16 * it) * S::LD + 32 * kk);
                         bf[p] = row_frag_of(brow + (p * C + 16 * jt) * S::LD + 32 * kk);
                     }
 #pragma unroll
@@ -771,7 +773,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 parts_of_pair<OP, F16, false>(y[2], y[3], w1);
 #pragma unroll
                 for (int p = 0; p < OP; ++p)
-                    *reinterpret_cast<u32x2 *>(&s.p[p][16 * it + oi][32 * (jt / 2) + 8 * og + 4 * (jt & 1)]) = u32x2{w0[p], w1[p]};
+                    *reinterpret_cast<u32x2 *>(&s.p[p][16 * it + oi][((4 * (jt / 2) + og) ^ S::swap(oi)) * 8 + 4 * (jt & 1)]) = u32x2{w0[p], w1[p]};
             }
 
             // What the rows read of the state.
@@ -794,7 +796,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     for (int it = 0; it < IT; ++it)
 #pragma unroll
                         for (int v = 0; v < IP; ++v) {
-                            const u32x4 af = row_frag(arow + (v * C + 16 * it) * S::LA + 32 * kk);
+                            const u32x4 af = row_frag(arow + (v * C + 16 * it) * S::LD + 32 * kk);
 #pragma unroll
                             for (int u = 0; u + v < OP; ++u)
                                 o[it] = mma<F16>(zf[u], af, o[it]);
@@ -818,7 +820,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         if constexpr (!STATES) {
             if (!SKIP || active) {
                 const int own = afresh(lane);
-                lds_u16 *const prow = (lds_u16 *)&s.p[0][0][0] + (own & 15) * S::LP + own / 16 * 8;
+                lds_u16 *const prow = (lds_u16 *)&s.p[0][0][0] + (own & 15) * S::LP;
+                const int piece = (own / 16) ^ S::swap(own & 15);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     u32x4 cf[IP];
@@ -829,7 +832,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     for (int it = 2 * ks; it < IT; ++it)
 #pragma unroll
                         for (int v = 0; v < OP; ++v) {
-                            const u32x4 pf = row_frag(prow + (v * C + 16 * it) * S::LP + 32 * ks);
+                            const u32x4 pf = row_frag(prow + (v * C + 16 * it) * S::LP + (piece ^ (4 * ks)) * 8);
 #pragma unroll
                             for (int u = 0; u < IP && u + v < OP; ++u)
                                 o[it] = mma<F16>(cf[u], pf, o[it]);
