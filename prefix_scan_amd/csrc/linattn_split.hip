@@ -553,12 +553,20 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     const Lines<T> la(sw.a, pl.seq, pl.first, head), lb(sw.b, pl.seq, pl.first, head),
         lc(sw.c, pl.seq, pl.first, head);
     Unit<T> ra[STATES ? 1 : N], rb[N], rc[N];
-    const auto fetch_chunk = [&](uint64_t at, int cnt) {
-        const uint64_t tok = rev ? pl.len - 1 - at : at;
+    const auto fetch_a = [&](uint64_t at, int cnt) {
         if constexpr (!STATES)
-            fetch<T, VEC, D, THREADS>(ra, la, tok, rev, cnt, m);
-        fetch<T, VEC, D, THREADS>(rb, lb, tok, rev, cnt, m);
-        fetch<T, VEC, D, THREADS>(rc, lc, tok, rev, cnt, n);
+            fetch<T, VEC, D, THREADS>(ra, la, rev ? pl.len - 1 - at : at, rev, cnt, m);
+    };
+    const auto fetch_b = [&](uint64_t at, int cnt) {
+        fetch<T, VEC, D, THREADS>(rb, lb, rev ? pl.len - 1 - at : at, rev, cnt, m);
+    };
+    const auto fetch_c = [&](uint64_t at, int cnt) {
+        fetch<T, VEC, D, THREADS>(rc, lc, rev ? pl.len - 1 - at : at, rev, cnt, n);
+    };
+    const auto fetch_chunk = [&](uint64_t at, int cnt) {
+        fetch_a(at, cnt);
+        fetch_b(at, cnt);
+        fetch_c(at, cnt);
     };
     uint64_t at = pl.lo, single = 0;   // tokens below `single` are taken one at a time
     int cnt = pl.hi - at < C ? (int)(pl.hi - at) : C, cnt_wt = -1, turn = 0;
@@ -719,11 +727,18 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         const uint64_t next = at + cnt;
         const uint64_t left = pl.hi - next;
         const int next_cnt = left == 0 ? 0 : next < single ? 1 : (int)(left < C ? left : C);
-        // The outputs of the chunk before go out ahead of these loads, which are
-        // waited for in order.
+        // The outputs of the chunk before go out ahead of the next one's rows,
+        // which are waited for in order.  These are asked for between the steps:
+        // all at once they fill the queue to memory, and the waves stand still
+        // for a third of the chunk's time.
         put_held();
-        if (next_cnt)
-            fetch_chunk(next, next_cnt);
+        if (next_cnt) {
+            fetch_a(next, next_cnt);
+            if constexpr (STATES) {
+                fetch_b(next, next_cnt);
+                fetch_c(next, next_cnt);
+            }
+        }
 
         // f16: scores are scaled by 2^rho, the state that is read by 2^tau.
         int rho = 0, tau = 0;
@@ -776,6 +791,9 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     *reinterpret_cast<u32x2 *>(&s.p[p][16 * it + oi][((4 * (jt / 2) + og) ^ S::swap(oi)) * 8 + 4 * (jt & 1)]) = u32x2{w0[p], w1[p]};
             }
 
+            if (next_cnt)
+                fetch_b(next, next_cnt);
+
             // What the rows read of the state.
 #pragma unroll
             for (int it = 0; it < IT; ++it)
@@ -813,6 +831,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                         o[it][r] *= w;
                 }
             }
+            if (next_cnt)
+                fetch_c(next, next_cnt);
             __syncthreads();
         }
 
