@@ -89,13 +89,20 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
 
 // Single tokens.  A workgroup has COLS = 4 LPR (or LPR) columns of one row's
 // and head's state: LPR lanes cover a row of them, 256 / LPR rows at a time,
-// so every load and store is 16 bytes a lane and the whole slab is in flight
-// at once.  Each thread adds up its rows' part of the output; the row groups
-// are added in LDS in a fixed order.
-template <class T, int V, int LPR>
+// so every load and store is 16 bytes a lane.  Each thread adds up its rows'
+// part of the output; the row groups are added in LDS in a fixed order.
+//
+// The state is read and written once, which bounds it: 256 rows of 32 heads
+// of 128 x 128 take 191 us, 5.6 TB/s (a copy: 6.8).  PAST: the state is past
+// what the caches hold from one step to the next, and is marked as such; all
+// of a thread's rows are then read at once.  Both ways, in us for 128, 192,
+// 256, 384 and 512 MiB: 43, 62, 89, 166, 214 kept, 51, 76, 98, 146, 196 past.
+// Four rows at a time are as fast as eight or 16 where it is kept (43, 43 and
+// 46 us for 128 MiB), the first four asked for before q and k.
+template <class T, int V, int LPR, bool PAST>
 __global__ __launch_bounds__(256) void step_kernel(const StepArgs a)
 {
-    constexpr int COLS = LPR * V, GROUPS = 256 / LPR;
+    constexpr int COLS = LPR * V, GROUPS = 256 / LPR, BATCH = PAST ? kLinattnWidth / GROUPS : 4;
     __shared__ float s_q[kLinattnWidth], s_k[kLinattnWidth];
     __shared__ float s_o[GROUPS][COLS];
     const uint32_t row = blockIdx.x, head = blockIdx.y;
@@ -109,6 +116,24 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs a)
             out[c0 + threadIdx.x] = (T)0.f;
         return;
     }
+    const uint64_t base = ((uint64_t)slot * a.heads + head) * ((uint64_t)a.dk * a.dv) + col;
+    const float *src = a.state + base;
+    float *dst = a.state_out + base;
+    const bool own = col < a.dv;
+    // The first rows are asked for ahead of all else.
+    typedef float Row __attribute__((ext_vector_type(V)));
+    Row x[BATCH];
+    const auto read = [&](int from) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int r = from + j * GROUPS;
+            if (!own || r >= a.dk)
+                continue;
+            const Row *at = reinterpret_cast<const Row *>(src + (int64_t)r * a.dv);
+            x[j] = PAST ? __builtin_nontemporal_load(at) : *at;
+        }
+    };
+    read(group);
     const T *q = row_ptr<T>(a.q, row, 0, head), *k = row_ptr<T>(a.k, row, 0, head);
     const T *v = row_ptr<T>(a.v, row, 0, head);
     if ((int)threadIdx.x < a.dk) {
@@ -116,9 +141,6 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs a)
         s_k[threadIdx.x] = to_f32(k[threadIdx.x]);
     }
     const Power w = decay_power(a.log_decay[head], 1.0);
-    const uint64_t base = ((uint64_t)slot * a.heads + head) * ((uint64_t)a.dk * a.dv) + col;
-    const float *src = a.state + base;
-    float *dst = a.state_out + base;
     float vv[V], o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -126,24 +148,26 @@ __global__ __launch_bounds__(256) void step_kernel(const StepArgs a)
         o[e] = 0.f;
     }
     __syncthreads();
-    if (col < a.dv) {
-#pragma unroll 4
-        for (int r = group; r < a.dk; r += GROUPS) {
-            float x[V];
-            if (V == 4)
-                *reinterpret_cast<f32x4 *>(x) = *reinterpret_cast<const f32x4 *>(src + (int64_t)r * a.dv);
-            else
-                x[0] = src[(int64_t)r * a.dv];
+    for (int from = group; from < a.dk; from += BATCH * GROUPS) {
+        if (from != group)
+            read(from);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int r = from + j * GROUPS;
+            if (!own || r >= a.dk)
+                continue;
             const float kr = s_k[r], qr = s_q[r];
+            Row y;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                x[e] = decayed(x[e], w) + kr * vv[e];
-                o[e] += qr * x[e];
+                y[e] = decayed(x[j][e], w) + kr * vv[e];
+                o[e] += qr * y[e];
             }
-            if (V == 4)
-                *reinterpret_cast<f32x4 *>(dst + (int64_t)r * a.dv) = *reinterpret_cast<f32x4 *>(x);
+            Row *at = reinterpret_cast<Row *>(dst + (int64_t)r * a.dv);
+            if (PAST)
+                __builtin_nontemporal_store(y, at);
             else
-                dst[(int64_t)r * a.dv] = x[0];
+                *at = y;
         }
     }
 #pragma unroll
@@ -167,13 +191,18 @@ void run_step(const StepArgs &a, hipStream_t stream)
     const auto blocks = [&](int cols) { return (unsigned)((a.dv + cols - 1) / cols); };
     // Narrow slabs where whole ones would leave compute units idle.
     const bool narrow = (uint64_t)a.rows * a.heads < 512;
+    const bool past = (uint64_t)a.rows * a.heads * a.dk * a.dv > (256u << 20) / sizeof(float);
     if (v == 4) {
         if (narrow)
-            step_kernel<T, 4, 8><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
+            step_kernel<T, 4, 8, false><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
+        else if (past)
+            step_kernel<T, 4, 32, true><<<dim3(a.rows, a.heads, blocks(128)), 256, 0, stream>>>(a);
         else
-            step_kernel<T, 4, 32><<<dim3(a.rows, a.heads, blocks(128)), 256, 0, stream>>>(a);
+            step_kernel<T, 4, 32, false><<<dim3(a.rows, a.heads, blocks(128)), 256, 0, stream>>>(a);
+    } else if (past) {
+        step_kernel<T, 1, 32, true><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
     } else {
-        step_kernel<T, 1, 32><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
+        step_kernel<T, 1, 32, false><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
     }
 }
 
