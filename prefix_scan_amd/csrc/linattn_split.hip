@@ -447,20 +447,31 @@ __device__ __forceinline__ void hold_rows(OutRows<T, D> &s, const f32x4 *o, int 
 // From there to memory, 16 bytes a lane.
 template <class T, int D, int THREADS>
 __device__ __forceinline__ void put_rows(OutRows<T, D> &s, T *out, int64_t tok, uint64_t at, bool rev, int cnt,
-                                         int n, bool aligned)
+                                         int n, int kind)
 {
     constexpr int C = In<T>::kChunk, V = OutRows<T, D>::V, PER = OutRows<T, D>::PIECES, RS = THREADS / PER;
     const int tid = afresh((int)threadIdx.x), row0 = tid / PER, piece = tid % PER, col = piece * V;
-    if (aligned && cnt == C) {
+    if (kind != kAnywhere && cnt == C) {
         char *base = reinterpret_cast<char *>(out + (int64_t)(rev ? at - (C - 1) : at) * tok);
         const int64_t step = (rev ? -RS : RS) * tok * (int64_t)sizeof(T);
         const uint32_t place =
             ((uint32_t)(rev ? C - 1 - row0 : row0) * (uint32_t)tok + (uint32_t)col) * (uint32_t)sizeof(T);
         if (col < n) {
+            const auto put = [&](auto past) {
 #pragma unroll
-            for (int k = 0; k < C / RS; ++k)
-                *reinterpret_cast<u32x4 *>(base + k * step + place) =
-                    *reinterpret_cast<const u32x4 *>(s.at(row0 + k * RS, piece));
+                for (int k = 0; k < C / RS; ++k) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(s.at(row0 + k * RS, piece));
+                    u32x4 *to = reinterpret_cast<u32x4 *>(base + k * step + place);
+                    if constexpr (past.value)
+                        __builtin_nontemporal_store(w, to);
+                    else
+                        *to = w;
+                }
+            };
+            if (kind == kPast)
+                put(std::true_type{});
+            else
+                put(std::false_type{});
         }
         return;
     }
@@ -663,7 +674,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         if constexpr (S::VIA)
             if (held_cnt)
                 put_rows<T, D, THREADS>(s.o, static_cast<T *>(sw.out) + out0, sw.out_tok, held_at, rev,
-                                        held_cnt, n, sw.out_aligned);
+                                        held_cnt, n, sw.out_kind);
         held_cnt = 0;
     };
     // This lane's places: along the rows of a, b and the scores, and down the
@@ -867,12 +878,12 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 const uint64_t tok = rev ? pl.len - 1 - at : at;
                 if (sizeof(T) == 2 && sw.out_f32)
                     put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, tok, rev, cnt,
-                                       wave * 16, n, sw.out_aligned);
+                                       wave * 16, n, sw.out_kind);
                 else if constexpr (S::VIA)
                     hold_rows<T, D, IT>(s.o, o, wave, l16, g4);
                 else
                     put_out<T, IT>(o, static_cast<T *>(sw.out) + out0, sw.out_tok, tok, rev, cnt, wave * 16,
-                                   n, sw.out_aligned);
+                                   n, sw.out_kind);
             }
             if (S::VIA && !(sizeof(T) == 2 && sw.out_f32)) {
                 held_at = rev ? pl.len - 1 - at : at;
