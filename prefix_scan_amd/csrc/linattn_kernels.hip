@@ -97,6 +97,8 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
 // what the caches hold from one step to the next, and is marked as such; all
 // of a thread's rows are then read at once.  Both ways, in us for 128, 192,
 // 256, 384 and 512 MiB: 43, 62, 89, 166, 214 kept, 51, 76, 98, 146, 196 past.
+// Rows that are no multiple of 16 bytes share their lines and are always kept
+// (484 MiB of 128 x 121: 371 us kept, 638 past).
 // Four rows at a time are as fast as eight or 16 where it is kept (43, 43 and
 // 46 us for 128 MiB), the first four asked for before q and k.
 template <class T, int V, int LPR, bool PAST>
@@ -199,8 +201,6 @@ void run_step(const StepArgs &a, hipStream_t stream)
             step_kernel<T, 4, 32, true><<<dim3(a.rows, a.heads, blocks(128)), 256, 0, stream>>>(a);
         else
             step_kernel<T, 4, 32, false><<<dim3(a.rows, a.heads, blocks(128)), 256, 0, stream>>>(a);
-    } else if (past) {
-        step_kernel<T, 1, 32, true><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
     } else {
         step_kernel<T, 1, 32, false><<<dim3(a.rows, a.heads, blocks(32)), 256, 0, stream>>>(a);
     }
