@@ -449,9 +449,10 @@ typedef struct {
  * a prefix scan of (decay, key_width x value_width matrix) pairs, in its
  * chunked form.  Sums and states are held in 32 bits.  bf16 rows are
  * multiplied as bf16, with the decayed scores and the state that a row reads
- * rounded to bf16; f16 rows as the sums of two bf16 parts, scores and state
- * rounded to two parts (2^-16).  State updates keep 24 bits of each decayed
- * row (16 where no final state is asked for).
+ * rounded to bf16 (2^-8); the state sums 24 bits of each decayed row (16 where
+ * no final state is asked for).  f16 rows are multiplied as f16, with scores,
+ * state and decayed rows, scaled by powers of two, in two f16 parts (2^-22).
+ * f32 rows, scores and state are three bf16 parts each (24 bits).
  *
  * state      device, [seqs][heads][key_width][value_width] floats: S before
  *            the first token, or NULL for zeros.

@@ -122,7 +122,6 @@ hipError_t launch_linattn_step(const StepArgs &a, hipStream_t stream);
 // ---------------------------------------------------------------------------
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // e^(g n) for n >= 0, with e^(g 0) = 1 for every g (a head without memory
 // has g = -inf), as the nearest float and what that leaves.  A state is

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
 // part of the output; the row groups are added in LDS in a fixed order.
 //
 // The state is read and written once, which bounds it: 256 rows of 32 heads
-// of 128 x 128 take 191 us, 5.6 TB/s (a copy: 6.8).  PAST: the state is past
+// of 128 x 128 take 196 us, 5.5 TB/s (a copy: 6.8).  PAST: the state is past
 // what the caches hold from one step to the next, and is marked as such; all
 // of a thread's rows are then read at once.  Both ways, in us for 128, 192,
 // 256, 384 and 512 MiB: 43, 62, 89, 166, 214 kept, 51, 76, 98, 146, 196 past.

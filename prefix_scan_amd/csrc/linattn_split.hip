@@ -12,8 +12,18 @@
 // so the state is read and written once a segment and every row of a, b and
 // c is read once.  The rows of chunk t + 1 are on their way in registers
 // while chunk t is computed from LDS.  16 columns a wave keep it at 128
-// registers, so that four waves a SIMD hide each other's waits: with 32
-// columns and two waves the same chunks took 1.5 times as long.
+// registers, so that four waves a SIMD hide each other's waits: 4 x 4096
+// tokens of 32 heads of 128 took 166 us with 32 columns a wave and half as
+// many waves, 130 with these (in segments, whose states are another 65).
+//
+// What bounds it.  That sweep moves 590 MB in 130 us, 4.5 TB/s (a copy: 6.8),
+// with 1.3 of 2.4 wave cycles waiting: each wave reads all rows of a and b
+// from LDS for its 16 columns, 512 bytes for each 16 x 16 x 32 product, and a
+// chunk's memory reads, LDS reads and products follow each other within a
+// workgroup; the two workgroups of a compute unit overlap them in part.  The
+// gradients' sweeps of 8 x 2048 x 16 take 197 us even with no rows read or
+// written; of those, 17 to 52 go with any one of the four steps, and 58 stay
+// without all of them.
 //
 // How exact.  An operand is one or more 16-bit parts whose products are
 // summed in 32 bits:
