@@ -448,9 +448,9 @@ typedef struct {
  *     S(t) = e^g S(t - 1) + k(t) v(t)^T,    out(t) = scale S(t)^T q(t),
  * a prefix scan of (decay, key_width x value_width matrix) pairs, in its
  * chunked form.  Sums and states are held in 32 bits.  bf16 rows are
- * multiplied as bf16, with the decayed scores and the state that a row reads
- * rounded to bf16 (2^-8); the state sums 24 bits of each decayed row (16 where
- * no final state is asked for).  f16 rows are multiplied as f16, with scores,
+ * multiplied as bf16, with 16 bits of the decayed scores and of the state that
+ * a row reads; the state sums 24 bits of each decayed row (16 where no final
+ * state is asked for).  f16 rows are multiplied as f16, with scores,
  * state and decayed rows, scaled by powers of two, in two f16 parts (2^-22).
  * f32 rows, scores and state are three bf16 parts each (24 bits).
  *

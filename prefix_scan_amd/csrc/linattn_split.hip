@@ -27,10 +27,14 @@
 //
 // How exact.  An operand is one or more 16-bit parts whose products are
 // summed in 32 bits:
-//   bf16 rows  are one part.  Scores and the state that a row reads are
-//              rounded to one (2^-8); the decayed rows that the state sums
-//              are cut into three, 24 bits, or two (2^-16) where no final
-//              state is asked for and the state is only read rounded.
+//   bf16 rows  are one part.  Scores and the state that a row reads are two,
+//              16 bits; the decayed rows that the state sums are three, 24
+//              bits, or two where no final state is asked for and the state
+//              is only read in two.  One part each, 2^-8, is seen in the
+//              outputs: 2.35e-3 from 64 bits in root mean square, where their
+//              own rounding, and two parts, are 1.66e-3.  It took 186, 432
+//              and 195 us, not 206, 467 and 228, for 4 x 4096 x 32 and
+//              65537 x 16 forward and the gradients of 8 x 2048 x 16.
 //   f16 rows   are one part of f16.  Scores, state and decayed rows leave
 //              f16's range, so each is scaled by a power of two taken from a
 //              bound of the chunk (largest exponents of its a, b and c; the
@@ -80,7 +84,7 @@ template <class T>
 struct In;
 template <>
 struct In<__bf16> {
-    static constexpr int kParts = 1, kMade = 1, kChunk = 64;
+    static constexpr int kParts = 1, kMade = 2, kChunk = 64;
     static constexpr bool kScaled = false;
 };
 template <>
@@ -500,12 +504,8 @@ __device__ __forceinline__ void put_rows(OutRows<T, D> &s, T *out, int64_t tok, 
     }
 }
 
-// VIA: outputs go through LDS, and out with the next chunk's loads; f16 rows
-// of 128 leave no room for that beside a second workgroup.
 template <class T, int D, bool STATES>
 struct Lds {
-    static constexpr bool VIA = !STATES && !(In<T>::kScaled && D == 128);
-    struct None {};
     static constexpr int C = In<T>::kChunk, IP = In<T>::kParts, OP = In<T>::kMade;
     static constexpr int LD = D + 16, LP = C == 64 ? 64 : C + 16;
     __device__ static constexpr int swap(int row) { return C == 64 ? (row >> 1 & 3) << 1 : 0; }
@@ -518,7 +518,13 @@ struct Lds {
     float wt[C];                           // pair_scale p^(cnt-1+shift-j)
     int bad[2];
     int exponent[2][4];                    // of a, b, c
-    alignas(16) typename std::conditional<VIA, OutRows<T, D>, None>::type o;
+    // A chunk's outputs take the place of its rows of a, which have been read by
+    // then: room of their own would leave one workgroup a compute unit.
+    __device__ __forceinline__ OutRows<T, D> &outputs()
+    {
+        static_assert(STATES || sizeof(OutRows<T, D>) <= sizeof(a), "outputs within a's rows");
+        return *reinterpret_cast<OutRows<T, D> *>(&a[0][0][0]);
+    }
 };
 
 // STATES: only the segment's own contribution to the state, into set.seg.
@@ -678,15 +684,6 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 
     const int64_t out0 = (int64_t)pl.seq * sw.out_seq + (int64_t)pl.first * sw.out_tok +
                          (int64_t)head * sw.out_head;
-    int held_cnt = 0;            // outputs in s.o, and their first token
-    uint64_t held_at = 0;
-    const auto put_held = [&]() {
-        if constexpr (S::VIA)
-            if (held_cnt)
-                put_rows<T, D, THREADS>(s.o, static_cast<T *>(sw.out) + out0, sw.out_tok, held_at, rev,
-                                        held_cnt, n, sw.out_kind);
-        held_cnt = 0;
-    };
     // This lane's places: along the rows of a, b and the scores, and down the
     // columns of b and c.
     lds_u16 *const arow = (lds_u16 *)&s.a[0][0][0] + l16 * S::LD + 8 * g4;
@@ -748,11 +745,9 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         const uint64_t next = at + cnt;
         const uint64_t left = pl.hi - next;
         const int next_cnt = left == 0 ? 0 : next < single ? 1 : (int)(left < C ? left : C);
-        // The outputs of the chunk before go out ahead of the next one's rows,
-        // which are waited for in order.  These are asked for between the steps:
-        // all at once they fill the queue to memory, and the waves stand still
-        // for a third of the chunk's time.
-        put_held();
+        // The next chunk's rows are asked for between the steps: all at once they
+        // fill the queue to memory, and the waves stand still for a third of the
+        // chunk's time.
         if (next_cnt) {
             fetch_a(next, next_cnt);
             if constexpr (STATES) {
@@ -859,6 +854,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 
         // What they read of the chunk's own tokens.
         if constexpr (!STATES) {
+            const uint64_t tok = rev ? pl.len - 1 - at : at;
             if (!SKIP || active) {
                 const int own = afresh(lane);
                 lds_u16 *const prow = (lds_u16 *)&s.p[0][0][0] + (own & 15) * S::LP;
@@ -885,19 +881,16 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     for (int it = 0; it < IT; ++it)
                         o[it] *= by;
                 }
-                const uint64_t tok = rev ? pl.len - 1 - at : at;
                 if (sizeof(T) == 2 && sw.out_f32)
                     put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, tok, rev, cnt,
                                        wave * 16, n, sw.out_kind);
-                else if constexpr (S::VIA)
-                    hold_rows<T, D, IT>(s.o, o, wave, l16, g4);
                 else
-                    put_out<T, IT>(o, static_cast<T *>(sw.out) + out0, sw.out_tok, tok, rev, cnt, wave * 16,
-                                   n, sw.out_kind);
+                    hold_rows<T, D, IT>(s.outputs(), o, wave, l16, g4);
             }
-            if (S::VIA && !(sizeof(T) == 2 && sw.out_f32)) {
-                held_at = rev ? pl.len - 1 - at : at;
-                held_cnt = cnt;
+            if (!(sizeof(T) == 2 && sw.out_f32)) {
+                __syncthreads();
+                put_rows<T, D, THREADS>(s.outputs(), static_cast<T *>(sw.out) + out0, sw.out_tok, tok, rev,
+                                        cnt, n, sw.out_kind);
             }
         }
         // The state past the chunk.
@@ -976,9 +969,6 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         cnt = next_cnt;
     }
 
-    if constexpr (S::VIA)
-        __syncthreads();
-    put_held();
     if (!active)
         return;
     if constexpr (F16) {
