@@ -1034,6 +1034,7 @@ int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const
         h.dst = rows_of(sh, *grad[i]);
         h.seqs = sh.ends ? 1 : sh.seqs;
         h.tokens = sh.tokens;
+        h.last_end = sh.ends ? sh.ends + sh.seqs - 1 : nullptr;
         h.heads = grad[i]->heads;
         h.share = sh.heads / grad[i]->heads;
         h.width = (int)width[i];

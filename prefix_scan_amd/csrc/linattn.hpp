@@ -94,11 +94,13 @@ hipError_t launch_sweeps(const SweepSet &set, hipStream_t stream);
 void launch_sweeps_split(const SweepSet &set, int width, hipStream_t stream);
 void launch_segment_scan(const SweepSet &set, int width, hipStream_t stream);
 
-// Sums the `share` consecutive heads of float rows into rows of `dtype`.
+// Sums the `share` consecutive heads of float rows into rows of `dtype`.  Of a
+// packed batch, the rows before the last end: no sweep has written the others.
 struct HeadSum {
     const float *src;            // [seqs][tokens][heads * share][width], dense
     Rows dst;                    // share unused
     uint64_t tokens, seqs;
+    const uint32_t *last_end;    // of a packed batch, or null
     uint32_t heads, share;
     int width, dtype;
 };

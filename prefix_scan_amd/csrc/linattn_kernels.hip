@@ -77,6 +77,8 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
     if (i >= h.seqs * h.tokens * per)
         return;
     const uint64_t row = i / per, head = i % per / h.width;
+    if (h.last_end && row >= *h.last_end)
+        return;
     const int c = (int)(i % h.width);
     const float *src = h.src + (row * h.heads + head) * h.share * h.width + c;
     float x = 0.f;
