@@ -24,7 +24,10 @@
  *   between calls (or it is freed and another allocation lands at the same
  *   address), call libscan_scratch_init on it before its next use.  Two calls
  *   that may run at the same time (different streams) need different scratch
- *   buffers.
+ *   buffers.  A call is a chain of kernels through its buffer: two host
+ *   threads must not be inside calls with the same buffer at once, on one
+ *   stream either, or their chains mix (the Python binding holds a lock for
+ *   each of its buffers).
  * Errors.  Every int-returning call returns LIBSCAN_OK (0) or a negative
  *   LIBSCAN_ERR_* code.  Argument errors are found before anything is
  *   launched and leave every buffer untouched.  LIBSCAN_ERR_HIP means a HIP

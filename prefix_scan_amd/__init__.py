@@ -219,11 +219,39 @@ def _stream_handle(device, stream):
 # --------------------------------------------------------------------------
 # Scratch: one zero-initialised buffer per (device, stream), grown on demand.
 # The library keeps a buffer consistent between calls by itself, so a buffer
-# is initialised only when it is created.
+# is initialised only when it is created.  A call is a chain of kernels through
+# its buffer, and host threads may share a stream: each call holds the buffer
+# (`with`) until all of its kernels are enqueued, so that chains follow one
+# another on the stream and never mix.
 # --------------------------------------------------------------------------
 _scratch = {}
 _outgrown = []          # kept: a captured graph may hold their addresses
-_scratch_lock = threading.Lock()
+
+
+class _Scratch:
+    """A stream's buffer; its lock is taken by _scratch_at and given back as the `with` ends."""
+    __slots__ = ("buf", "lock")
+
+    def __init__(self):
+        self.buf, self.lock = None, threading.Lock()
+
+    def __enter__(self):
+        return self.buf
+
+    def __exit__(self, *exc):
+        self.lock.release()
+
+    def grow(self, device, stream_obj, nbytes):
+        old = self.buf
+        size = max(nbytes, 2 * old.numel() if old is not None else 0, 1 << 16)
+        with torch.cuda.stream(stream_obj):
+            buf = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(lib().libscan_scratch_init(ctypes.c_void_p(buf.data_ptr()), size,
+                                          ctypes.c_void_p(stream_obj.cuda_stream)),
+               "libscan_scratch_init")
+        if old is not None:
+            _outgrown.append(old)
+        self.buf = buf
 
 
 # The current stream's handle, by the short way where this torch has it.
@@ -232,28 +260,22 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 
 def _scratch_at(device, index, handle, stream, nbytes):
-    """_scratch_for, by the stream's handle: a buffer that is large enough is found at once."""
-    buf = _scratch.get((index, handle))
-    if buf is None or buf.numel() < nbytes:
-        buf = _scratch_for(device, stream or torch.cuda.current_stream(device), nbytes)
-    return buf
+    """The buffer of a stream (by its handle) of at least nbytes, held: for a `with`."""
+    held = _scratch.get((index, handle))
+    if held is None:
+        held = _scratch.setdefault((index, handle), _Scratch())
+    held.lock.acquire()
+    try:
+        if held.buf is None or held.buf.numel() < nbytes:
+            held.grow(device, stream or torch.cuda.current_stream(device), nbytes)
+    except BaseException:
+        held.lock.release()
+        raise
+    return held
 
 
 def _scratch_for(device, stream_obj, nbytes):
-    key = (device.index, stream_obj.cuda_stream)
-    with _scratch_lock:
-        buf = _scratch.get(key)
-        if buf is None or buf.numel() < nbytes:
-            size = max(nbytes, 2 * buf.numel() if buf is not None else 0, 1 << 16)
-            with torch.cuda.stream(stream_obj):
-                buf = torch.empty(size, dtype=torch.uint8, device=device)
-            _check(lib().libscan_scratch_init(ctypes.c_void_p(buf.data_ptr()), size,
-                                              ctypes.c_void_p(stream_obj.cuda_stream)),
-                   "libscan_scratch_init")
-            if key in _scratch:
-                _outgrown.append(_scratch[key])
-            _scratch[key] = buf
-        return buf
+    return _scratch_at(device, device.index, stream_obj.cuda_stream, stream_obj, nbytes)
 
 
 def _ptr(t):
@@ -292,20 +314,20 @@ def scan_u32_ex(data, inclusive=False, algo="auto", fork_depth=-1, want_total=Tr
     a = _algo(algo)
     sh, s = _stream_handle(data.device, stream)
     need = lib().scan_ex_scratch_bytes(data.numel(), a, fork_depth)
-    scr = _scratch_for(data.device, s, need)
-    host, hp = _total_args(want_total, total_dev)
-    _check(lib().scan_u32_ex(_ptr(data), data.numel(), 1 if inclusive else 0, a, fork_depth, hp,
-                             _ptr(total_dev), _ptr(scr), scr.numel(), sh), "scan_u32_ex")
+    with _scratch_for(data.device, s, need) as scr:
+        host, hp = _total_args(want_total, total_dev)
+        _check(lib().scan_u32_ex(_ptr(data), data.numel(), 1 if inclusive else 0, a, fork_depth, hp,
+                                 _ptr(total_dev), _ptr(scr), scr.numel(), sh), "scan_u32_ex")
     return int(host.value) if want_total else None
 
 
 def _scan(name, data, want_total, total_dev, stream):
     _dev_u32(data, "data")
     sh, s = _stream_handle(data.device, stream)
-    scr = _scratch_for(data.device, s, lib().scan_scratch_bytes(data.numel()))
-    host, hp = _total_args(want_total, total_dev)
-    _check(getattr(lib(), name)(_ptr(data), data.numel(), hp, _ptr(total_dev), _ptr(scr),
-                                scr.numel(), sh), name)
+    with _scratch_for(data.device, s, lib().scan_scratch_bytes(data.numel())) as scr:
+        host, hp = _total_args(want_total, total_dev)
+        _check(getattr(lib(), name)(_ptr(data), data.numel(), hp, _ptr(total_dev), _ptr(scr),
+                                    scr.numel(), sh), name)
     return int(host.value) if want_total else None
 
 
@@ -328,10 +350,10 @@ def scan_op_u32(data, op, inclusive=False, want_total=True, total_dev=None, stre
     _dev_u32(data, "data")
     o = _op(op)
     sh, s = _stream_handle(data.device, stream)
-    scr = _scratch_for(data.device, s, lib().scan_scratch_bytes(data.numel()))
-    host, hp = _total_args(want_total, total_dev)
-    _check(lib().scan_op_u32(_ptr(data), data.numel(), o, 1 if inclusive else 0, hp,
-                             _ptr(total_dev), _ptr(scr), scr.numel(), sh), "scan_op_u32")
+    with _scratch_for(data.device, s, lib().scan_scratch_bytes(data.numel())) as scr:
+        host, hp = _total_args(want_total, total_dev)
+        _check(lib().scan_op_u32(_ptr(data), data.numel(), o, 1 if inclusive else 0, hp,
+                                 _ptr(total_dev), _ptr(scr), scr.numel(), sh), "scan_op_u32")
     return int(host.value) if want_total else None
 
 
@@ -341,10 +363,10 @@ def reduce_op_u32(data, op, want_total=True, total_dev=None, stream=None):
     _dev_u32(data, "data")
     o = _op(op)
     sh, s = _stream_handle(data.device, stream)
-    scr = _scratch_for(data.device, s, lib().reduce_scratch_bytes(data.numel()))
-    host, hp = _total_args(want_total, total_dev)
-    _check(lib().reduce_op_u32(_ptr(data), data.numel(), o, hp, _ptr(total_dev), _ptr(scr),
-                               scr.numel(), sh), "reduce_op_u32")
+    with _scratch_for(data.device, s, lib().reduce_scratch_bytes(data.numel())) as scr:
+        host, hp = _total_args(want_total, total_dev)
+        _check(lib().reduce_op_u32(_ptr(data), data.numel(), o, hp, _ptr(total_dev), _ptr(scr),
+                                   scr.numel(), sh), "reduce_op_u32")
     return int(host.value) if want_total else None
 
 
@@ -363,10 +385,10 @@ def scan_op_u64(data, op, inclusive=False, want_total=True, total_dev=None, stre
     _dev_u64(data, "data")
     o = _op(op)
     sh, s = _stream_handle(data.device, stream)
-    scr = _scratch_for(data.device, s, lib().scan_op_u64_scratch_bytes(data.numel()))
-    host, hp = _total64_args(want_total, total_dev)
-    _check(lib().scan_op_u64(_ptr(data), data.numel(), o, 1 if inclusive else 0, hp,
-                             _ptr(total_dev), _ptr(scr), scr.numel(), sh), "scan_op_u64")
+    with _scratch_for(data.device, s, lib().scan_op_u64_scratch_bytes(data.numel())) as scr:
+        host, hp = _total64_args(want_total, total_dev)
+        _check(lib().scan_op_u64(_ptr(data), data.numel(), o, 1 if inclusive else 0, hp,
+                                 _ptr(total_dev), _ptr(scr), scr.numel(), sh), "scan_op_u64")
     return int(host.value) if want_total else None
 
 
@@ -376,10 +398,10 @@ def reduce_op_u64(data, op, want_total=True, total_dev=None, stream=None):
     _dev_u64(data, "data")
     o = _op(op)
     sh, s = _stream_handle(data.device, stream)
-    scr = _scratch_for(data.device, s, lib().reduce_scratch_bytes(data.numel()))
-    host, hp = _total64_args(want_total, total_dev)
-    _check(lib().reduce_op_u64(_ptr(data), data.numel(), o, hp, _ptr(total_dev), _ptr(scr),
-                               scr.numel(), sh), "reduce_op_u64")
+    with _scratch_for(data.device, s, lib().reduce_scratch_bytes(data.numel())) as scr:
+        host, hp = _total64_args(want_total, total_dev)
+        _check(lib().reduce_op_u64(_ptr(data), data.numel(), o, hp, _ptr(total_dev), _ptr(scr),
+                                   scr.numel(), sh), "reduce_op_u64")
     return int(host.value) if want_total else None
 
 
@@ -405,10 +427,10 @@ def runs_layout_u32(counts, ends=None, want_entries=True, entries_dev=None, stre
     if ends.numel() != n:
         raise ValueError("ends must have as many elements as counts")
     sh, s = _stream_handle(counts.device, stream)
-    scr = _scratch_for(counts.device, s, lib().runs_scratch_bytes(n, 0))
-    host, hp = _total_args(want_entries, entries_dev)
-    _check(lib().runs_layout_u32(_ptr(counts), _ptr(ends), n, hp, _ptr(entries_dev), _ptr(scr),
-                                 scr.numel(), sh), "runs_layout_u32")
+    with _scratch_for(counts.device, s, lib().runs_scratch_bytes(n, 0)) as scr:
+        host, hp = _total_args(want_entries, entries_dev)
+        _check(lib().runs_layout_u32(_ptr(counts), _ptr(ends), n, hp, _ptr(entries_dev), _ptr(scr),
+                                     scr.numel(), sh), "runs_layout_u32")
     return ends, (int(host.value) if want_entries else None)
 
 
@@ -432,9 +454,9 @@ def runs_owner_u32(ends, entry, owner=None, stream=None):
     if owner.numel() != entry.numel():
         raise ValueError("owner must have as many elements as entry")
     sh, s = _stream_handle(entry.device, stream)
-    scr = _scratch_for(entry.device, s, lib().runs_scratch_bytes(ends.numel(), 0))
-    _check(lib().runs_owner_u32(_ptr(ends), ends.numel(), _ptr(entry), entry.numel(), _ptr(owner),
-                                _ptr(scr), scr.numel(), sh), "runs_owner_u32")
+    with _scratch_for(entry.device, s, lib().runs_scratch_bytes(ends.numel(), 0)) as scr:
+        _check(lib().runs_owner_u32(_ptr(ends), ends.numel(), _ptr(entry), entry.numel(), _ptr(owner),
+                                    _ptr(scr), scr.numel(), sh), "runs_owner_u32")
     return owner
 
 
@@ -447,9 +469,9 @@ def runs_owner_all_u32(ends, total, owner=None, stream=None):
     if owner.numel() != total:
         raise ValueError("owner must have `total` elements")
     sh, s = _stream_handle(ends.device, stream)
-    scr = _scratch_for(ends.device, s, lib().runs_scratch_bytes(ends.numel(), total))
-    _check(lib().runs_owner_all_u32(_ptr(ends), ends.numel(), _ptr(owner), total, _ptr(scr),
-                                    scr.numel(), sh), "runs_owner_all_u32")
+    with _scratch_for(ends.device, s, lib().runs_scratch_bytes(ends.numel(), total)) as scr:
+        _check(lib().runs_owner_all_u32(_ptr(ends), ends.numel(), _ptr(owner), total, _ptr(scr),
+                                        scr.numel(), sh), "runs_owner_all_u32")
     return owner
 
 
@@ -479,9 +501,9 @@ def segscan_u32(inp, seg_len, out=None, seg_sums=True, stream=None):
         if seg_sums.numel() < (n + seg_len - 1) // seg_len:
             raise ValueError("seg_sums needs ceil(n / seg_len) entries")
     sh, s = _stream_handle(inp.device, stream)
-    scr = _scratch_for(inp.device, s, lib().segscan_scratch_bytes(n, seg_len))
-    _check(lib().segscan_u32(_ptr(inp), _ptr(out), n, seg_len, _ptr(seg_sums), _ptr(scr),
-                             scr.numel(), sh), "segscan_u32")
+    with _scratch_for(inp.device, s, lib().segscan_scratch_bytes(n, seg_len)) as scr:
+        _check(lib().segscan_u32(_ptr(inp), _ptr(out), n, seg_len, _ptr(seg_sums), _ptr(scr),
+                                 scr.numel(), sh), "segscan_u32")
     return out, seg_sums
 
 
@@ -511,11 +533,11 @@ def segscan_flags_u32(inp, flags, out=None, seg_sums=True, want_nsegs=True, nseg
     if seg_sums is not None:
         _dev_u32(seg_sums, "seg_sums")
     sh, s = _stream_handle(inp.device, stream)
-    scr = _scratch_for(inp.device, s, lib().segscan_flags_scratch_bytes(n))
-    host, hp = _total_args(want_nsegs, nsegs_dev)
-    _check(lib().segscan_flags_u32(_ptr(inp), _ptr(flags), _ptr(out), n, _ptr(seg_sums), hp,
-                                   _ptr(nsegs_dev), _ptr(scr), scr.numel(), sh),
-           "segscan_flags_u32")
+    with _scratch_for(inp.device, s, lib().segscan_flags_scratch_bytes(n)) as scr:
+        host, hp = _total_args(want_nsegs, nsegs_dev)
+        _check(lib().segscan_flags_u32(_ptr(inp), _ptr(flags), _ptr(out), n, _ptr(seg_sums), hp,
+                                       _ptr(nsegs_dev), _ptr(scr), scr.numel(), sh),
+               "segscan_flags_u32")
     nsegs = int(host.value) if want_nsegs else None
     if made and nsegs is not None:
         seg_sums = seg_sums[:nsegs]
@@ -537,10 +559,10 @@ def compact_flags_u32(flags, out=None, want_count=True, count_dev=None, stream=N
     if out.numel() != n:
         raise ValueError("out must have as many elements as flags")
     sh, s = _stream_handle(flags.device, stream)
-    scr = _scratch_for(flags.device, s, lib().compact_scratch_bytes(n))
-    host, hp = _total_args(want_count, count_dev)
-    _check(lib().compact_flags_u32(_ptr(flags), _ptr(out), n, hp, _ptr(count_dev), _ptr(scr),
-                                   scr.numel(), sh), "compact_flags_u32")
+    with _scratch_for(flags.device, s, lib().compact_scratch_bytes(n)) as scr:
+        host, hp = _total_args(want_count, count_dev)
+        _check(lib().compact_flags_u32(_ptr(flags), _ptr(out), n, hp, _ptr(count_dev), _ptr(scr),
+                                       scr.numel(), sh), "compact_flags_u32")
     return out, (int(host.value) if want_count else None)
 
 
@@ -558,9 +580,9 @@ def radix_perm_u32(keys, bits_per_pass=1, perm=None, stream=None):
     if perm.numel() != n:
         raise ValueError("perm must have as many elements as keys")
     sh, s = _stream_handle(keys.device, stream)
-    scr = _scratch_for(keys.device, s, lib().radix_scratch_bytes(n, bits_per_pass))
-    _check(lib().radix_perm_u32(_ptr(keys), _ptr(perm), n, bits_per_pass, _ptr(scr), scr.numel(),
-                                sh), "radix_perm_u32")
+    with _scratch_for(keys.device, s, lib().radix_scratch_bytes(n, bits_per_pass)) as scr:
+        _check(lib().radix_perm_u32(_ptr(keys), _ptr(perm), n, bits_per_pass, _ptr(scr), scr.numel(),
+                                    sh), "radix_perm_u32")
     return perm
 
 
@@ -590,9 +612,9 @@ def copy_u32(src, dst, stream=None):
     if dst.numel() != src.numel():
         raise ValueError("src and dst differ in size")
     sh, s = _stream_handle(src.device, stream)
-    scr = _scratch_for(src.device, s, lib().copy_scratch_bytes(src.numel()))
-    _check(lib().copy_u32(_ptr(src), _ptr(dst), src.numel(), _ptr(scr), scr.numel(), sh),
-           "copy_u32")
+    with _scratch_for(src.device, s, lib().copy_scratch_bytes(src.numel())) as scr:
+        _check(lib().copy_u32(_ptr(src), _ptr(dst), src.numel(), _ptr(scr), scr.numel(), sh),
+               "copy_u32")
     return dst
 
 
@@ -788,9 +810,9 @@ def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=Fal
     if state_out is None and want_state:
         state_out = p.new_states()
     handle = p.stream(stream)
-    scr = p.scratch(handle, stream)
-    _check(lib().linattn(p.shape(ends, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v), _addr(state),
-                         p.at(3, out), _addr(state_out), scr.data_ptr(), scr.numel(), handle), "linattn")
+    with p.scratch(handle, stream) as scr:
+        _check(lib().linattn(p.shape(ends, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v), _addr(state),
+                             p.at(3, out), _addr(state_out), scr.data_ptr(), scr.numel(), handle), "linattn")
     return out, state_out
 
 
@@ -822,11 +844,11 @@ def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dst
     if dstate is None and want_dstate:
         dstate = p.new_states()
     handle = p.stream(stream)
-    scr = p.scratch(handle, stream)
-    _check(lib().linattn_grad(p.shape(ends, log_decay, scale), p.at(0, dout), p.at(1, q), p.at(2, k),
-                              p.at(3, v), _addr(state), _addr(dstate_out), p.at(4, dq), p.at(5, dk),
-                              p.at(6, dv), _addr(dstate), scr.data_ptr(), scr.numel(), handle),
-           "linattn_grad")
+    with p.scratch(handle, stream) as scr:
+        _check(lib().linattn_grad(p.shape(ends, log_decay, scale), p.at(0, dout), p.at(1, q), p.at(2, k),
+                                  p.at(3, v), _addr(state), _addr(dstate_out), p.at(4, dq), p.at(5, dk),
+                                  p.at(6, dv), _addr(dstate), scr.data_ptr(), scr.numel(), handle),
+               "linattn_grad")
     return dq, dk, dv, dstate
 
 
@@ -912,6 +934,6 @@ def sample_logits(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
                 _addr(each[0]), _addr(each[2]), _addr(each[3]), _addr(each[1]),
                 tokens.data_ptr(), logprobs.data_ptr(), kept.data_ptr())
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    scr = _scratch_at(device, index, handle, stream, need)
-    _check(lib().sample_logits(a, scr.data_ptr(), scr.numel(), handle), "sample_logits")
+    with _scratch_at(device, index, handle, stream, need) as scr:
+        _check(lib().sample_logits(a, scr.data_ptr(), scr.numel(), handle), "sample_logits")
     return tokens, logprobs, kept
