@@ -97,6 +97,11 @@ const char *libscan_version(void);
  * the header once its start is rounded up to 256 bytes. */
 int libscan_scratch_init(void *scratch, size_t scratch_bytes, hipStream_t stream);
 
+/* 1 if a call with this scratch buffer has been recorded into a HIP graph,
+ * which may be replayed as long as it lives: the buffer has to live as long.
+ * 0 if none has. */
+int libscan_scratch_captured(const void *scratch, size_t scratch_bytes);
+
 /* ------------------------------------------------------------------------ */
 /* Scan                                                                     */
 /* ------------------------------------------------------------------------ */

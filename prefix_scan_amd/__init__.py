@@ -103,6 +103,8 @@ def lib():
         L.libscan_version.restype = ctypes.c_char_p
         L.libscan_scratch_init.argtypes = [vp, sz, vp]
         L.libscan_scratch_init.restype = i32
+        L.libscan_scratch_captured.argtypes = [vp, sz]
+        L.libscan_scratch_captured.restype = i32
         L.scan_scratch_bytes.argtypes = [u64]
         L.scan_scratch_bytes.restype = sz
         L.scan_ex_scratch_bytes.argtypes = [u64, i32, i32]
@@ -225,7 +227,8 @@ def _stream_handle(device, stream):
 # another on the stream and never mix.
 # --------------------------------------------------------------------------
 _scratch = {}
-_outgrown = []          # kept: a captured graph may hold their addresses
+_outgrown = []          # kept: buffers that a captured graph may hold
+_DOUBLED = 1 << 28      # larger buffers grow to the need, smaller ones to twice their size
 
 
 class _Scratch:
@@ -242,15 +245,20 @@ class _Scratch:
         self.lock.release()
 
     def grow(self, device, stream_obj, nbytes):
-        old = self.buf
-        size = max(nbytes, 2 * old.numel() if old is not None else 0, 1 << 16)
+        size = max(nbytes, 1 << 16)
+        if self.buf is not None:
+            if size < _DOUBLED:
+                size = max(size, 2 * self.buf.numel())
+            if lib().libscan_scratch_captured(_ptr(self.buf), self.buf.numel()):
+                _outgrown.append(self.buf)
+            # The work that is under way in it is ahead, on the stream that it
+            # goes back to.
+            self.buf = None
         with torch.cuda.stream(stream_obj):
             buf = torch.empty(size, dtype=torch.uint8, device=device)
         _check(lib().libscan_scratch_init(ctypes.c_void_p(buf.data_ptr()), size,
                                           ctypes.c_void_p(stream_obj.cuda_stream)),
                "libscan_scratch_init")
-        if old is not None:
-            _outgrown.append(old)
         self.buf = buf
 
 

@@ -442,8 +442,17 @@ int libscan_scratch_init(void *scratch, size_t scratch_bytes, hipStream_t stream
     hipError_t e = launch_fill_zero(s.base, kHeaderBytes, stream);
     if (e != hipSuccess)
         return hip_status(e);
-    g_states.zeroed((uintptr_t)s.base);
+    g_states.zeroed((uintptr_t)s.base, stream_capturing(stream));
     return LIBSCAN_OK;
+}
+
+int libscan_scratch_captured(const void *scratch, size_t scratch_bytes)
+{
+    Scratch s;
+    return scratch && carve(const_cast<void *>(scratch), scratch_bytes, 0, &s) &&
+                   g_states.captured((uintptr_t)s.base)
+               ? 1
+               : 0;
 }
 
 size_t scan_scratch_bytes(uint64_t n)

@@ -128,10 +128,19 @@ public:
         records_.erase(key);
     }
 
-    // libscan_scratch_init: header zeroed, no body byte trusted.
-    void zeroed(uintptr_t key)
+    // Whether a call on the buffer has been recorded into a graph.
+    bool captured(uintptr_t key)
     {
         std::lock_guard<std::mutex> lock(mu_);
+        return captured_.count(key) != 0;
+    }
+
+    // libscan_scratch_init: header zeroed, no body byte trusted.
+    void zeroed(uintptr_t key, bool capturing = false)
+    {
+        std::lock_guard<std::mutex> lock(mu_);
+        if (capturing)
+            captured_.insert(key);
         records_[key] = StateRecord{kKindZero, 0, 0, 0};
     }
 
