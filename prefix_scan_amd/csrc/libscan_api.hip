@@ -320,16 +320,15 @@ SweepSet sweep_set(const linattn_shape_t &s, int count)
     set.heads = s.heads;
     set.tokens = s.tokens;
     set.seg_len = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count, widest(s));
+    set.slots = (uint32_t)linattn_slots(s.tokens, s.ends != nullptr, s.seqs, set.seg_len);
     set.items = (uint32_t)linattn_items(s.tokens, s.ends != nullptr, s.seqs, set.seg_len);
     return set;
 }
 
 size_t segment_bytes(const linattn_shape_t &s, int count)
 {
-    const SweepSet set = sweep_set(s, count);
-    if (!set.seg_len)
-        return 0;
-    return round_up((size_t)count * set.items * s.heads * linattn_state_floats(widest(s)) * sizeof(float),
+    return round_up((size_t)count * sweep_set(s, count).slots * s.heads * linattn_state_floats(widest(s)) *
+                        sizeof(float),
                     kScratchAlign);
 }
 

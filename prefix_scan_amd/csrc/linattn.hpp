@@ -20,8 +20,9 @@
 //
 // A sequence is cut into segments of seg_len tokens, one workgroup each, so
 // that few long sequences still fill the GPU: a first kernel sums every
-// segment's own contribution to the state, a second scans those sums along
-// the sequence, and the third sweeps each segment from its entering state.
+// segment's own contribution to the state (but the last's, which none reads),
+// a second scans those sums along the sequence, and the third sweeps each
+// segment from its entering state.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -76,16 +77,19 @@ struct SweepSet {
     uint64_t tokens;             // of each sequence, or in all when ends is given
     uint64_t seg_len;            // 0: sequences are not cut
     uint32_t items;              // workgroups along the tokens
-    float *seg;                  // segment states (when seg_len != 0)
+    uint32_t slots;              // states of segments, of each head and sweep
+    float *seg;                  // [sweeps][slots][heads] of them
     bool aligned;                // every row starts on 16 bytes and is a whole number of them
 };
 
-// Tokens per segment for a set of sweeps (0: no cutting) and the number of
-// (sequence, segment) items a grid has to cover.
+// Tokens per segment for a set of sweeps (0: no cutting), the number of
+// segments with others after them, which have a state each, and that of the
+// items a grid has to cover.
 uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps,
                          int width);
+uint64_t linattn_slots(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len);
 uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len);
-// Floats of segment states one item of one head of one sweep takes.
+// Floats of a segment's state.
 size_t linattn_state_floats(int width);
 
 hipError_t launch_sweeps(const SweepSet &set, hipStream_t stream);
@@ -160,19 +164,9 @@ struct Place {
     uint64_t first;      // token of the packed batch the sequence starts at (0 when dense)
     uint64_t len;        // tokens of the sequence
     uint64_t lo, hi;     // the segment, in the sweep's order
+    uint32_t slot0;      // where the state of the sequence's first segment is
     bool last;
 };
-
-__device__ __forceinline__ uint32_t wave_incl_u32(uint32_t x)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t y = __shfl_up(x, d);
-        if ((int)(threadIdx.x & 63) >= d)
-            x += y;
-    }
-    return x;
-}
 
 // Sequence i of a packed batch.  Ends past the batch, or falling ones, are
 // cut to it, so that no list of ends reaches outside the rows.
@@ -185,53 +179,63 @@ __device__ __forceinline__ void run_of(const uint32_t *ends, uint64_t tokens, ui
     *len = b > a ? b - a : 0;
 }
 
-// Every sequence has max(1, ceil(len / seg_len)) items, in order.  False: the
-// item is past the last one.  One wave reads 64 run ends at a time.
-__device__ __forceinline__ bool place_of(const SweepSet &set, uint32_t item, Place *p)
+// The first of the ascending `ends` above x, or `n`.  One wave, 64 at a time.
+__device__ __forceinline__ uint32_t first_above(const uint32_t *ends, uint32_t n, uint64_t x)
+{
+    uint32_t at = 0;
+    while (n) {
+        // Lane l looks at the last of the l-th `step`.
+        const uint32_t step = (n + 63) / 64, whole = n / step, l = threadIdx.x & 63;
+        const uint64_t hit = __ballot(l < whole && ends[at + (l < whole ? l : 0) * step + step - 1] > x);
+        const uint32_t skip = hit ? (uint32_t)__ffsll((unsigned long long)hit) - 1 : whole;
+        at += skip * step;
+        n = hit ? step - 1 : n - whole * step;
+    }
+    return at;
+}
+
+// A sequence of n > 1 segments has n - 1 slots, from slot0 on, for the states
+// of all but the last.  In a packed batch, a segment of L tokens holds one
+// multiple of L among the batch's tokens, and that over L is its slot: so a
+// slot's sequence is found by its token, and slots and items do not depend on
+// where sequences end.  Items are each sequence's last segment, then the
+// slots'; those of a dense batch are all segments in order.  `cut`: only what
+// has a slot, where states are summed.  False: the item has no segment.
+__device__ __forceinline__ bool place_of(const SweepSet &set, uint32_t item, bool cut, Place *p)
 {
     const uint64_t L = set.seg_len;
-    uint64_t s;
+    uint64_t s = 0, segs = 1;
     if (!set.ends) {
-        const uint64_t n = L && set.tokens ? (set.tokens + L - 1) / L : 1;
-        p->seq = (uint32_t)(item / n);
-        s = item % n;
         p->first = 0;
         p->len = set.tokens;
+        segs = L && p->len ? (p->len + L - 1) / L : 1;
+        const uint64_t n = cut ? segs - 1 : segs;
+        p->seq = (uint32_t)(item / n);
+        s = item % n;
+        p->slot0 = p->seq * (uint32_t)(segs - 1);
         if (p->seq >= set.seqs)
             return false;
-    } else if (!L) {
-        if (item >= set.seqs)
+    } else if (cut || item >= set.seqs) {
+        const uint32_t slot = cut ? item : item - set.seqs;
+        const uint64_t x = slot * L;
+        if (slot >= set.slots)
             return false;
-        p->seq = item;
-        s = 0;
-        run_of(set.ends, set.tokens, item, &p->first, &p->len);
-    } else {
-        uint32_t before = 0;
-        bool found = false;
-        s = 0;
-        for (uint32_t i0 = 0; i0 < set.seqs && !found; i0 += 64) {
-            const uint32_t i = i0 + (threadIdx.x & 63);
-            uint64_t first = 0, len = 0;
-            uint32_t n = 0;
-            if (i < set.seqs) {
-                run_of(set.ends, set.tokens, i, &first, &len);
-                n = len ? (uint32_t)((len + L - 1) / L) : 1u;
-            }
-            const uint32_t incl = wave_incl_u32(n);
-            const uint64_t hit = __ballot(before + incl > item);
-            if (hit) {
-                const int src = __ffsll((unsigned long long)hit) - 1;
-                p->seq = i0 + src;
-                s = item - (before + __shfl(incl - n, src));
-                found = true;
-            }
-            before += __shfl(incl, 63);
-        }
-        if (!found)
+        p->seq = first_above(set.ends, set.seqs, x);
+        if (p->seq >= set.seqs)
             return false;
         run_of(set.ends, set.tokens, p->seq, &p->first, &p->len);
+        p->slot0 = (uint32_t)((p->first + L - 1) / L);
+        s = slot - p->slot0;
+        if (x < p->first || (s + 1) * L >= p->len)
+            return false;
+    } else {
+        p->seq = item;
+        run_of(set.ends, set.tokens, p->seq, &p->first, &p->len);
+        p->slot0 = L ? (uint32_t)((p->first + L - 1) / L) : 0;
+        segs = L && p->len ? (p->len + L - 1) / L : 1;
+        s = segs - 1;
     }
-    p->lo = L ? s * L : 0;
+    p->lo = s * L;
     p->hi = L && p->lo + L < p->len ? p->lo + L : p->len;
     p->last = p->hi == p->len;
     return true;

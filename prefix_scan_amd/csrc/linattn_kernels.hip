@@ -12,58 +12,39 @@ namespace {
 template <class T>
 __device__ __forceinline__ float to_f32(T x) { return (float)x; }
 
-// The exclusive scan of a sequence's segment states, (l, S) o (r, U) =
-// (l r, r S + U), each thread four elements of the state: segment s is left
-// with what its tokens read of the segments before it.
+// The scan of a sequence's segment states, (l, S) o (r, U) = (l r, r S + U),
+// each thread four elements of the state: a segment's slot is left with what
+// the next one reads.  The workgroups of a sequence's first slot do it.
 template <int D>
 __global__ __launch_bounds__(256) void segment_scan_kernel(const SweepSet set)
 {
     const uint32_t head = blockIdx.y;
     constexpr uint32_t PARTS = D * D / 1024;
-    const uint32_t sweep = blockIdx.z, seq = blockIdx.x / PARTS;
+    const uint32_t sweep = blockIdx.z;
     const uint64_t L = set.seg_len;
-    uint64_t first = 0, len = set.tokens, item = 0;
-    if (!set.ends) {
-        item = (uint64_t)seq * ((set.tokens + L - 1) / L);
-    } else {
-        run_of(set.ends, set.tokens, seq, &first, &len);
-        if (len <= L)
-            return;
-        for (uint32_t i0 = 0; i0 < seq; i0 += 64) {
-            const uint32_t i = i0 + (threadIdx.x & 63);
-            uint32_t n = 0;
-            if (i < seq) {
-                uint64_t f, l;
-                run_of(set.ends, set.tokens, i, &f, &l);
-                n = l ? (uint32_t)((l + L - 1) / L) : 1u;
-            }
-            item += __shfl(wave_incl_u32(n), 63);
-        }
-    }
-    if (len <= kFewSegments * L)
+    Place pl;
+    if (!place_of(set, blockIdx.x / PARTS, true, &pl) || pl.lo != 0 || pl.len <= kFewSegments * L)
         return;
-    const uint64_t segs = (len + L - 1) / L;
-    if (item + segs > set.items)        // ends that no batch of this many tokens has
-        return;
+    const uint64_t slots = (pl.len + L - 1) / L - 1;
     const Power w = decay_power(set.log_decay[head], (double)L);
     f32x4 *p = reinterpret_cast<f32x4 *>(
-                   set.seg + (((uint64_t)sweep * set.items + item) * set.heads + head) * (D * D)) +
+                   set.seg + (((uint64_t)sweep * set.slots + pl.slot0) * set.heads + head) * (D * D)) +
                blockIdx.x % PARTS * 256 + threadIdx.x;
     const uint64_t step = (uint64_t)set.heads * (D * D) / 4;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     constexpr int AHEAD = 8;            // loads in flight ahead of the chain
-    for (uint64_t s = 0; s < segs; s += AHEAD) {
+    for (uint64_t s = 0; s < slots; s += AHEAD) {
         f32x4 own[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i)      // the last segment left no sum
-            own[i] = s + i + 1 < segs ? p[(s + i) * step] : f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < AHEAD; ++i)
+            own[i] = s + i < slots ? p[(s + i) * step] : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
-            if (s + i < segs) {
-                p[(s + i) * step] = sum;
+            if (s + i < slots) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     sum[e] = decayed(sum[e], w) + own[i][e];
+                p[(s + i) * step] = sum;
             }
     }
 }
@@ -240,16 +221,22 @@ uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t h
     return segs > 1 ? ((tokens + segs - 1) / segs + 63) / 64 * 64 : 0;
 }
 
-uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len)
+uint64_t linattn_slots(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len)
 {
     if (!seg_len)
-        return seqs;
-    return ragged ? seqs + tokens / seg_len : seqs * ((tokens + seg_len - 1) / seg_len);
+        return 0;
+    // A token is left behind the last segment that has a slot.
+    return ragged ? (tokens - 1 + seg_len - 1) / seg_len : seqs * ((tokens + seg_len - 1) / seg_len - 1);
+}
+
+uint64_t linattn_items(uint64_t tokens, bool ragged, uint32_t seqs, uint64_t seg_len)
+{
+    return seqs + linattn_slots(tokens, ragged, seqs, seg_len);
 }
 
 void launch_segment_scan(const SweepSet &set, int width, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(width * width / 1024) * set.seqs, set.heads, (unsigned)set.count);
+    const dim3 grid((unsigned)(width * width / 1024) * set.slots, set.heads, (unsigned)set.count);
     if (width == 64)
         segment_scan_kernel<64><<<grid, 256, 0, stream>>>(set);
     else

@@ -547,8 +547,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     // go round them), so that its cache has the rows for all.
     uint32_t sweep = 0, item = blockIdx.x, head = blockIdx.y;
     if (set.count > 1) {
-        const uint64_t units = (uint64_t)set.items * set.heads, n = units / 8 * 8 * set.count;
-        const uint64_t b = item + set.items * (head + (uint64_t)set.heads * blockIdx.z);
+        const uint64_t units = (uint64_t)gridDim.x * set.heads, n = units / 8 * 8 * set.count;
+        const uint64_t b = item + gridDim.x * (head + (uint64_t)set.heads * blockIdx.z);
         uint64_t unit;
         if (b < n) {
             sweep = (uint32_t)(b / 8 % set.count);
@@ -557,21 +557,27 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             sweep = (uint32_t)((b - n) % set.count);
             unit = units / 8 * 8 + (b - n) / set.count;
         }
-        item = (uint32_t)(unit % set.items);
-        head = (uint32_t)(unit / set.items);
+        item = (uint32_t)(unit % gridDim.x);
+        head = (uint32_t)(unit / gridDim.x);
+    } else if (set.ends) {
+        // Sequences differ in length: each one's heads go round the dies, so
+        // that these have equal shares.  37 prompts of 600 tokens on average,
+        // 24 heads, f16: 204 us; 220 to 320 by items, as their number has it.
+        const uint64_t b = blockIdx.x + (uint64_t)gridDim.x * blockIdx.y;
+        item = uniform((uint32_t)(b / set.heads));
+        head = uniform((uint32_t)(b % set.heads));
     }
     const Sweep &sw = set.s[sweep];
     Place pl;
-    if (!place_of(set, item, &pl))
+    if (!place_of(set, item, STATES, &pl))
         return;
     pl.seq = uniform(pl.seq);
     pl.first = uniform64(pl.first);
     pl.len = uniform64(pl.len);
     pl.lo = uniform64(pl.lo);
     pl.hi = uniform64(pl.hi);
+    pl.slot0 = uniform(pl.slot0);
     pl.last = pl.hi == pl.len;
-    if (STATES && pl.last)
-        return;
     const int wave = uniform(threadIdx.x / 64);
     const int lane = threadIdx.x & 63, g4 = lane >> 4, l16 = lane & 15;
     const float g = set.log_decay[head];
@@ -629,18 +635,18 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             z[kk][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto seg_of = [&](uint32_t at) {
-        return set.seg + (((uint64_t)sweep * set.items + at) * set.heads + head) * (D * D) +
+    const auto seg_of = [&](uint32_t slot) {
+        return set.seg + (((uint64_t)sweep * set.slots + slot) * set.heads + head) * (D * D) +
                (wave * KK * 64 + lane) * 8;
     };
     if (!STATES && active) {
         if (pl.lo) {
             // The scan's result, or the scan itself where segments are few.
             const bool few = pl.len <= kFewSegments * set.seg_len;
-            const uint32_t before = few ? (uint32_t)(pl.lo / set.seg_len) : 1;
+            const uint32_t before = (uint32_t)(pl.lo / set.seg_len);
             const Power w = decay_power(g, (double)set.seg_len);
-            for (uint32_t k = 0; k < before; ++k) {
-                const float *seg = seg_of(few ? item - before + k : item);
+            for (uint32_t k = few ? 0 : before - 1; k < before; ++k) {
+                const float *seg = seg_of(pl.slot0 + k);
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -980,7 +986,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 z[kk][u] *= by;
     }
     if (STATES) {
-        float *seg = seg_of(item);
+        float *seg = seg_of(pl.slot0 + (uint32_t)(pl.lo / set.seg_len));
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -1003,8 +1009,9 @@ template <class T, int D, bool VEC, int WP>
 void run_split(const SweepSet &set, hipStream_t stream)
 {
     const dim3 grid(set.items, set.heads, (unsigned)set.count);
-    if (set.seg_len) {
-        sweep_split_kernel<T, D, VEC, WP, true><<<grid, D * 4, 0, stream>>>(set);
+    if (set.slots) {
+        const dim3 cut(set.slots, set.heads, (unsigned)set.count);
+        sweep_split_kernel<T, D, VEC, WP, true><<<cut, D * 4, 0, stream>>>(set);
         if (set.tokens > kFewSegments * set.seg_len)
             launch_segment_scan(set, D, stream);
     }
