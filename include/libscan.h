@@ -471,7 +471,8 @@ typedef struct {
  * Nothing at a token that is in no sequence is read; a value that is not
  * finite reaches no earlier token and no other sequence.
  * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type, widths, heads), ERR_SIZE
- * (more than LIBSCAN_MAX_N tokens, or a grid too large), ERR_SCRATCH, ERR_HIP.
+ * (more than LIBSCAN_MAX_N tokens or 65535 heads; 2^24 sequences, 2^23 where a
+ * width is above 64), ERR_SCRATCH, ERR_HIP.
  */
 size_t linattn_scratch_bytes(const linattn_shape_t *shape);
 int linattn(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
@@ -503,6 +504,7 @@ int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const
  * state      device, [pool][heads][key_width][value_width] floats.
  * state_out  where the new states go: `state` itself, or a pool that does
  *            not overlap it (slots of no row are left as they are).
+ * Errors as for linattn; ERR_SIZE from 2^24 rows on.
  */
 int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
                  const linattn_rows_t *v, const float *state, uint64_t pool, const int32_t *slots,

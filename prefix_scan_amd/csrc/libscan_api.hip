@@ -332,10 +332,14 @@ size_t segment_bytes(const linattn_shape_t &s, int count)
                     kScratchAlign);
 }
 
+// Threads of a grid's side: 2^32 are refused by the launch, and by the checks
+// before anything is launched.
+bool past_a_grid(uint64_t groups, unsigned threads) { return groups * threads > 0xFFFFFFFFull; }
+
 bool too_many_items(const linattn_shape_t &s, int count)
 {
     const uint64_t l = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count, widest(s));
-    return linattn_items(s.tokens, s.ends != nullptr, s.seqs, l) > (1u << 26);
+    return past_a_grid(linattn_items(s.tokens, s.ends != nullptr, s.seqs, l), widest(s) <= 64 ? 256 : 512);
 }
 
 uint64_t all_rows(const linattn_shape_t &s) { return s.ends ? s.tokens : s.tokens * s.seqs; }
@@ -1070,6 +1074,8 @@ int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const li
         return LIBSCAN_ERR_ALIGN;
     if (!any)
         return LIBSCAN_OK;
+    if (past_a_grid(sh.seqs, 256))
+        return LIBSCAN_ERR_SIZE;
     if (!sh.log_decay || ((!state || !state_out) && pool != 0))
         return LIBSCAN_ERR_NULL;
     if (pool > LIBSCAN_MAX_N)

@@ -54,20 +54,20 @@ template <class T>
 __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
 {
     const uint64_t per = (uint64_t)h.heads * h.width;
-    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= h.seqs * h.tokens * per)
-        return;
-    const uint64_t row = i / per, head = i % per / h.width;
-    if (h.last_end && row >= *h.last_end)
-        return;
-    const int c = (int)(i % h.width);
-    const float *src = h.src + (row * h.heads + head) * h.share * h.width + c;
-    float x = 0.f;
-    for (uint32_t k = 0; k < h.share; ++k)
-        x += src[(uint64_t)k * h.width];
-    T *dst = static_cast<T *>(const_cast<void *>(h.dst.p));
-    dst[(int64_t)(row / h.tokens) * h.dst.seq + (int64_t)(row % h.tokens) * h.dst.tok +
-        (int64_t)head * h.dst.head + c] = (T)x;
+    const uint64_t all = h.seqs * h.tokens * per;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (uint64_t)gridDim.x * 256) {
+        const uint64_t row = i / per, head = i % per / h.width;
+        if (h.last_end && row >= *h.last_end)
+            return;
+        const int c = (int)(i % h.width);
+        const float *src = h.src + (row * h.heads + head) * h.share * h.width + c;
+        float x = 0.f;
+        for (uint32_t k = 0; k < h.share; ++k)
+            x += src[(uint64_t)k * h.width];
+        T *dst = static_cast<T *>(const_cast<void *>(h.dst.p));
+        dst[(int64_t)(row / h.tokens) * h.dst.seq + (int64_t)(row % h.tokens) * h.dst.tok +
+            (int64_t)head * h.dst.head + c] = (T)x;
+    }
 }
 
 // Single tokens.  A workgroup has COLS = 4 LPR (or LPR) columns of one row's
@@ -260,7 +260,8 @@ hipError_t launch_head_sum(const HeadSum &h, hipStream_t stream)
     const uint64_t n = h.seqs * h.tokens * h.heads * (uint64_t)h.width;
     if (n == 0)
         return hipSuccess;
-    const unsigned blocks = (unsigned)((n + 255) / 256);
+    // A grid holds fewer than 2^32 threads.
+    const unsigned blocks = (unsigned)(n < ((uint64_t)1 << 31) ? (n + 255) / 256 : 1u << 23);
     switch (h.dtype) {
     case LIBSCAN_F32: head_sum_kernel<float><<<blocks, 256, 0, stream>>>(h); break;
     case LIBSCAN_BF16: head_sum_kernel<__bf16><<<blocks, 256, 0, stream>>>(h); break;
