@@ -436,8 +436,9 @@ typedef struct {
  * ends NULL: `seqs` sequences of `tokens` tokens each.  Else device, `seqs`
  * u32 (what runs_layout_u32 leaves): the sequences lie one after another in
  * `tokens` rows, sequence s at tokens [ends[s - 1], ends[s]); seq_stride is
- * not used.  Ends beyond `tokens`, or that fall, are cut to what lies inside;
- * outputs of tokens in no sequence are not written.
+ * not used.  Ends beyond `tokens` count as `tokens`; outputs of tokens past the
+ * last end are not written.  Ends that fall are no batch: what then is in the
+ * outputs and states is unspecified, and nothing else is read or written.
  * log_decay: device, `heads` floats g, at most 0 in use: what a head's state
  * keeps of itself from token to token is e^g (-inf: no memory).  The decays
  * are constants of the model: there is no gradient for them.

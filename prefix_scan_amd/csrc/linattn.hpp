@@ -168,8 +168,10 @@ struct Place {
     bool last;
 };
 
-// Sequence i of a packed batch.  Ends past the batch, or falling ones, are
-// cut to it, so that no list of ends reaches outside the rows.
+// Sequence i of a packed batch.  Ends past the batch are cut to it and a
+// sequence that ends before it starts has no tokens, so that no list of ends
+// reaches outside the rows.  With falling ends two sequences may hold the same
+// rows, and a slot may be left as it was.
 __device__ __forceinline__ void run_of(const uint32_t *ends, uint64_t tokens, uint32_t i,
                                        uint64_t *first, uint64_t *len)
 {
