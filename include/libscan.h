@@ -459,9 +459,10 @@ typedef struct {
  * chunked form.  Sums and states are held in 32 bits.  bf16 rows are
  * multiplied as bf16, with 16 bits of the decayed scores and of the state that
  * a row reads; the state sums 24 bits of each decayed row (16 where no final
- * state is asked for).  f16 rows are multiplied as f16, with scores,
- * state and decayed rows, scaled by powers of two, in two f16 parts (2^-22).
- * f32 rows, scores and state are three bf16 parts each (24 bits).
+ * state is asked for).  f16 rows are multiplied as f16, with scores, state and
+ * decayed rows, scaled by powers of two, in two f16 parts: 2^-22, and at least
+ * 2^-40 of the largest score of the token, number of the state's 16 columns or
+ * decayed row of 64.  f32 rows, scores and state are three bf16 parts each (24 bits).
  *
  * state      device, [seqs][heads][key_width][value_width] floats: S before
  *            the first token, or NULL for zeros.

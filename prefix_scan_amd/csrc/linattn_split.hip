@@ -36,10 +36,15 @@
 //              and 195 us, not 206, 467 and 228, for 4 x 4096 x 32 and
 //              65537 x 16 forward and the gradients of 8 x 2048 x 16.
 //   f16 rows   are one part of f16.  Scores, state and decayed rows leave
-//              f16's range, so each is scaled by a power of two taken from a
-//              bound of the chunk (largest exponents of its a, b and c; the
-//              state's bound follows its recurrence) and scaled back in 32
-//              bits; they are two parts each (2^-22).
+//              f16's range, so they are scaled by powers of two and back in 32
+//              bits: each row of scores by its own largest (no row sees what
+//              another holds), the state by the largest of a wave's 16 columns,
+//              the decayed rows by the largest of those whose b is not zeros.
+//              They are two parts each: 2^-22 of a number, or 2^-40 of what it
+//              is scaled by where that is more.  The rows' scales cost a
+//              barrier and a second look at the scores: 226 us for 37 prompts
+//              of 600 tokens on average, 24 heads, 203 with one scale a chunk,
+//              which loses ordinary rows beside large ones.
 //   f32 rows   are three bf16 parts, 24 bits, as are scores, state and
 //              decayed rows; of the nine products the six above 2^-24 are
 //              taken, at a rate 2.7 times the 32-bit products'.
@@ -62,6 +67,7 @@
 #include "linattn.hpp"
 
 #include "../../include/libscan.h"
+#include "device_common.hpp"
 
 #include <type_traits>
 
@@ -111,10 +117,21 @@ __device__ __forceinline__ float value16(uint32_t w, int high)
         return high ? high16(w) : low16(w);
 }
 
-// Two floats' upper halves in one word: both cut to bf16.
+// a's and b's lower, and upper, halves in one word.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b)
+{
+    return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
+
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b)
+{
+    return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+
+// Two floats, both cut to bf16.
 __device__ __forceinline__ uint32_t cut_pair(float a, float b)
 {
-    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    return high_halves(__float_as_uint(a), __float_as_uint(b));
 }
 
 template <bool F16>
@@ -290,7 +307,7 @@ template <class T, bool PERMUTED, int W, int THREADS, int N, int CH, int LD>
 __device__ __forceinline__ void stage(const Unit<T> (&r)[N], uint16_t (*dst)[CH][LD])
 {
     constexpr int PER = W / 8, RS = THREADS / PER;
-    const int row0 = threadIdx.x / PER, unit = threadIdx.x % PER;
+    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, unit = tid % PER;
     const int col = PERMUTED ? unit / 4 * 32 + (unit & 1) * 16 + (unit & 2) * 2 : unit * 8;
     const auto put = [&](int part, int row, u32x4 w) {
         uint16_t *p = &dst[part][row][col];
@@ -332,41 +349,57 @@ __device__ __forceinline__ bool any_not_finite(const Unit<T> (&r)[N])
                 const uint32_t w = r[k].w[h][e];
                 if constexpr (sizeof(T) == 4)
                     bad |= (w & 0x7F800000u) + 0x00800000u;
+                else if constexpr (In<T>::kScaled)
+                    bad |= (w & 0x7C007C00u) + 0x04000400u;
                 else
                     bad |= (w & 0x7F807F80u) + 0x00800080u;
             }
     return (bad & (sizeof(T) == 4 ? 0x80000000u : 0x80008000u)) != 0;
 }
 
-// The largest of a wave's numbers in [0, 2 TOP).
-template <int TOP>
-__device__ __forceinline__ int wave_most(int own)
+// The largest of a wave's numbers.
+__device__ __forceinline__ uint32_t wave_most(uint32_t x)
 {
-    int most = 0;
-#pragma unroll
-    for (int b = TOP; b; b >>= 1)
-        if (__any(own >= most + b))
-            most += b;
-    return most;
+    const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    x = larger(x, dpp<kDppRowShr1, 0xF>(x));
+    x = larger(x, dpp<kDppRowShr2, 0xF>(x));
+    x = larger(x, dpp<kDppRowShr4, 0xF>(x));
+    x = larger(x, dpp<kDppRowShr8, 0xF>(x));
+    x = larger(x, dpp<kDppRowBcast15, 0xA>(x));
+    x = larger(x, dpp<kDppRowBcast31, 0xC>(x));
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 
-// The largest biased exponent among a wave's f16 values (31: not finite).
-template <class T, int N>
-__device__ __forceinline__ int wave_exponent(const Unit<T> (&r)[N])
+// The largest exponent that a decayed row of c has among this thread's rows of
+// f16: |x| < 2^(the returned - 140).  Rows whose b is zeros add nothing to the
+// state and do not count.  pw: the power of the chunk's first row, those of
+// the next before it.
+template <class T, int W, int THREADS, int N>
+__device__ __forceinline__ int decayed_exponent(const Unit<T> (&b)[N], const Unit<T> (&c)[N], const float *pw,
+                                                float scale, int cnt)
 {
-    uint32_t lo = 0, hi = 0;
+    constexpr int PER = W / 8, RS = THREADS / PER;
+    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, lane = tid & 63;
+    int most = 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int k = 0; k < N; ++k) {
+        uint32_t any = 0, lo = 0, hi = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t l = r[k].w[0][e] & 0x7C00u, h = r[k].w[0][e] & 0x7C000000u;
+            any |= b[k].w[0][e];
+            const uint32_t l = c[k].w[0][e] & 0x7FFFu, h = c[k].w[0][e] & 0x7FFF0000u;
             lo = l > lo ? l : lo;
             hi = h > hi ? h : hi;
         }
-    lo >>= 10;
-    hi >>= 26;
-    const int own = (int)(lo > hi ? lo : hi);
-    return wave_most<16>(own);
+        const uint64_t rows = __ballot((any & 0x7FFF7FFFu) != 0) >> (lane / PER * PER);
+        const uint32_t top = lo > hi >> 16 ? lo : hi >> 16;
+        const int row = row0 + k * RS;
+        if ((rows & ((1u << PER) - 1)) != 0 && top != 0 && row < cnt) {
+            const int e = (int)(top >> 10) + (int)(__float_as_uint(scale * pw[-row]) >> 23 & 255);
+            most = e > most ? e : most;
+        }
+    }
+    return most;
 }
 
 // LDS by its own pointers: a lane's place plus a constant, which the
@@ -400,11 +433,17 @@ __device__ __forceinline__ u32x4 row_frag_of(lds_u16 *p)
 
 __device__ __forceinline__ float power2(int e)
 {
-    return __builtin_amdgcn_ldexpf(1.f, e < -120 ? -120 : e > 120 ? 120 : e);
+    return __builtin_amdgcn_ldexpf(1.f, e < -126 ? -126 : e > 126 ? 126 : e);
 }
 
-// e with |x| < 2^e.
-__device__ __forceinline__ int above_exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 126; }
+// The power of two that takes a row's scores, the largest of them with the bits
+// `most`, to below 2^15.  Not past 2^40: scores below 2^-26 lie below f16's
+// outputs whatever the rows of c are.
+__device__ __forceinline__ int row_scale(uint32_t most)
+{
+    const int e = (int)(most >> 23);
+    return e == 255 ? 0 : e < 101 ? 40 : 141 - e;
+}
 
 // This lane's row and four of the 16 columns from `first` of each tile.
 template <class T, int IT>
@@ -517,7 +556,8 @@ struct Lds {
     float pair[C + 16];                    // pair_scale out_scale p^d at 16 + d, 0 for d < 0
     float wt[C];                           // pair_scale p^(cnt-1+shift-j)
     int bad[2];
-    int exponent[2][4];                    // of a, b, c
+    int top[2];                            // f16: decayed_exponent of the chunk
+    uint32_t most[In<T>::kScaled && !STATES ? C : 1];   // bits of each row's largest score
     // A chunk's outputs take the place of its rows of a, which have been read by
     // then: room of their own would leave one workgroup a compute unit.
     __device__ __forceinline__ OutRows<T, D> &outputs()
@@ -604,7 +644,6 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
     uint64_t at = pl.lo, single = 0;   // tokens below `single` are taken one at a time
     int cnt = pl.hi - at < C ? (int)(pl.hi - at) : C, cnt_wt = -1, turn = 0;
     double whole = 1.0, drift = 1.0;   // p^cnt; what the factors so far left of it
-    float wt_max = 0.f, wt_sum = 0.f;
     fetch_chunk(at, cnt);
     for (int i = threadIdx.x; i < C + 17; i += THREADS) {
         const int d = i - 16;
@@ -616,11 +655,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             s.pl[d] = p.lo;
         }
     }
-    if (threadIdx.x < 2) {
-        s.bad[threadIdx.x] = 0;
-        for (int i = 0; i < 4; ++i)
-            s.exponent[threadIdx.x][i] = 0;
-    }
+    if (threadIdx.x < 2)
+        s.bad[threadIdx.x] = s.top[threadIdx.x] = 0;
     if constexpr (!STATES)                  // the scores' upper corner stays zero
         for (int i = threadIdx.x; i < OP * C * S::LP / 8; i += THREADS)
             reinterpret_cast<u32x4 *>(&s.p[0][0][0])[i] = u32x4{0, 0, 0, 0};
@@ -671,22 +707,32 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 }
         }
     }
-    // f16: z holds the state times 2^sigma, whose absolute values are below bound.
+    // f16: z holds the state times 2^sigma.  top_of_z: the exponent of the
+    // largest number that is finite in it.
     int sigma = 0;
-    float bound = 0.f;
-    const auto find_bound = [&]() {
-        float own = 0.f;
+    const auto top_of_z = [&]() {
+        uint32_t own = 0;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float x = __builtin_fabsf(z[kk][e / 4][e % 4]);
-                own = x > own && x < __builtin_inff() ? x : own;
+                const uint32_t x = __float_as_uint(z[kk][e / 4][e % 4]) & 0x7FFFFFFFu;
+                own = x > own ? x : own;
             }
-        bound = power2(wave_most<128>(own > 0.f ? above_exponent(own) + 126 : 0) - 126 - sigma);
+        own = wave_most(own);
+        if (own >= 0x7F800000u) {
+            own = 0;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t x = __float_as_uint(z[kk][e / 4][e % 4]) & 0x7FFFFFFFu;
+                    own = x > own && x < 0x7F800000u ? x : own;
+                }
+            own = wave_most(own);
+        }
+        return (int)(own >> 23);
     };
-    if constexpr (F16 && !STATES)
-        find_bound();
 
     const int64_t out0 = (int64_t)pl.seq * sw.out_seq + (int64_t)pl.first * sw.out_tok +
                          (int64_t)head * sw.out_head;
@@ -702,46 +748,29 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             stage<T, true, D, THREADS>(ra, s.a);
         stage<T, false, D, THREADS>(rb, s.b);
         stage<T, false, D, THREADS>(rc, s.c);
+        if (__any(any_not_finite(rc)) && lane == 0)
+            s.bad[turn] = 1;
         if constexpr (F16) {
-            int e[3] = {0, wave_exponent(rb), wave_exponent(rc)};
-            if constexpr (!STATES)
-                e[0] = wave_exponent(ra);
-            if (lane < 3)
-                atomicMax(&s.exponent[turn][lane], lane == 0 ? e[0] : lane == 1 ? e[1] : e[2]);
-        } else {
-            if (__any(any_not_finite(rc)) && lane == 0)
-                s.bad[turn] = 1;
+            const int top = (int)wave_most((uint32_t)decayed_exponent<T, D, THREADS>(
+                rb, rc, &s.pw[cnt - 1 + sw.shift], sw.pair_scale, cnt));
+            if (lane == 0)
+                atomicMax(&s.top[turn], top);
+            if (!STATES && threadIdx.x < C)
+                s.most[threadIdx.x] = 0;
         }
         if (cnt != cnt_wt) {
             const int j = afresh((int)threadIdx.x);
             if (j < C)
                 s.wt[j] = j < cnt ? sw.pair_scale * s.pw[cnt - 1 + sw.shift - j] : 0.f;
-            if constexpr (F16) {
-                // Their largest, and a bound of their sum.
-                wt_max = uniform_float(__builtin_fabsf(sw.pair_scale) *
-                                       fmaxf(s.pw[cnt - 1 + sw.shift], s.pw[sw.shift]));
-                const float far = 1.f / (1.f - s.pw[1]);
-                wt_sum = uniform_float(wt_max * (far > 0.f && far < cnt ? far : (float)cnt));
-            }
             cnt_wt = cnt;
             whole = uniform_double((double)s.pw[cnt] + (double)s.pl[cnt]);
         }
         __syncthreads();
-        int ea = 0, eb = 0, ec = 0;
-        bool bad;
-        if constexpr (F16) {
-            ea = (int)uniform(s.exponent[turn][0]);
-            eb = (int)uniform(s.exponent[turn][1]);
-            ec = (int)uniform(s.exponent[turn][2]);
-            bad = ea == 31 || eb == 31 || ec == 31;
-        } else {
-            bad = uniform(s.bad[turn]) != 0;
-        }
+        const bool bad = uniform(s.bad[turn]) != 0;
+        const int top = F16 ? (int)uniform(s.top[turn]) : 0;
         turn ^= 1;
         if (threadIdx.x == 0)
-            s.bad[turn] = 0;
-        if (F16 && threadIdx.x < 3)
-            s.exponent[turn][threadIdx.x] = 0;
+            s.bad[turn] = s.top[turn] = 0;
         if (bad && cnt > 1) {          // again, one token at a time
             single = at + cnt;
             cnt = 1;
@@ -762,22 +791,16 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             }
         }
 
-        // f16: scores are scaled by 2^rho, the state that is read by 2^tau.
-        int rho = 0, tau = 0;
-        if constexpr (F16) {
-            const float most = fmaxf(__builtin_fabsf(s.pair[16]), __builtin_fabsf(s.pair[16 + C - 1]));
-            rho = 15 - (ea + eb - 28 + 7 + (int)uniform((uint32_t)above_exponent(most)));
-            rho = rho < -40 ? -40 : rho > 40 ? 40 : rho;
-            tau = 15 - above_exponent(bound);
-        }
+        int top_z = 0;
         f32x4 o[IT];
         if constexpr (!STATES) {
             // Scores, transposed: a lane has token i and four consecutive j.
             const int own = afresh(lane), oi = own & 15, og = own / 16;
             lds_u16 *const brow = (lds_u16 *)&s.b[0][0][0] + oi * S::LD + 4 * og;
-#pragma unroll 1
-            for (int x = wave; x < IT * (IT + 1) / 2; x += NW) {
-                const int it = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, jt = x - it * (it + 1) / 2;
+            constexpr int TILES = IT * (IT + 1) / 2;
+            const auto row_of = [](int x) { return x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3; };
+            const auto scores = [&](int x) {
+                const int it = row_of(x), jt = x - it * (it + 1) / 2;
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
@@ -796,21 +819,57 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                             acc = mma<F16>(bf[u], af[v], acc);
                 }
                 const int d0 = 16 * (it - jt) + oi - 4 * og;
-                float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[e] = acc[e] * s.pair[16 + d0 - e];
-                    if constexpr (F16)
-                        y[e] *= power2(rho);
-                    if (d0 - e < 0)
-                        y[e] = 0.f;
-                }
+                for (int e = 0; e < 4; ++e)
+                    acc[e] = d0 - e < 0 ? 0.f : acc[e] * s.pair[16 + d0 - e];
+                return acc;
+            };
+            // This lane's four of a tile, in each part.
+            const auto place = [&](int p, int x) {
+                const int it = row_of(x), jt = x - it * (it + 1) / 2;
+                return reinterpret_cast<u32x2 *>(
+                    &s.p[p][16 * it + oi][((4 * (jt / 2) + og) ^ S::swap(oi)) * 8 + 4 * (jt & 1)]);
+            };
+            const auto put_scores = [&](int x, f32x4 y) {
                 uint32_t w0[OP], w1[OP];
                 parts_of_pair<OP, F16, false>(y[0], y[1], w0);
                 parts_of_pair<OP, F16, false>(y[2], y[3], w1);
 #pragma unroll
                 for (int p = 0; p < OP; ++p)
-                    *reinterpret_cast<u32x2 *>(&s.p[p][16 * it + oi][((4 * (jt / 2) + og) ^ S::swap(oi)) * 8 + 4 * (jt & 1)]) = u32x2{w0[p], w1[p]};
+                    *place(p, x) = u32x2{w0[p], w1[p]};
+            };
+            if constexpr (F16) {
+                // Each row by its own power of two, so that it has what it would
+                // have without the others.  Until that is known the scores' 32
+                // bits wait in the places of the two parts: in registers over
+                // the barrier they cost spills.
+#pragma unroll 1
+                for (int x = wave; x < TILES; x += NW) {
+                    const f32x4 y = scores(x);
+                    uint32_t b[4], most = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        b[e] = __float_as_uint(y[e]);
+                        most = (b[e] & 0x7FFFFFFFu) > most ? b[e] & 0x7FFFFFFFu : most;
+                    }
+                    atomicMax(&s.most[16 * row_of(x) + oi], most);
+                    *place(0, x) = u32x2{low_halves(b[0], b[1]), low_halves(b[2], b[3])};
+                    *place(1, x) = u32x2{high_halves(b[0], b[1]), high_halves(b[2], b[3])};
+                }
+                __syncthreads();
+#pragma unroll 1
+                for (int x = wave; x < TILES; x += NW) {
+                    const u32x2 lo = *place(0, x), hi = *place(1, x);
+                    const f32x4 y = {__uint_as_float(low_halves(lo[0], hi[0])),
+                                     __uint_as_float(high_halves(lo[0], hi[0])),
+                                     __uint_as_float(low_halves(lo[1], hi[1])),
+                                     __uint_as_float(high_halves(lo[1], hi[1]))};
+                    put_scores(x, y * power2(row_scale(s.most[16 * row_of(x) + oi])));
+                }
+            } else {
+#pragma unroll 1
+                for (int x = wave; x < TILES; x += NW)
+                    put_scores(x, scores(x));
             }
 
             if (next_cnt)
@@ -821,7 +880,13 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             for (int it = 0; it < IT; ++it)
                 o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
             if (!SKIP || active) {
-                const float by = F16 ? power2(tau - sigma) : 1.f;
+                // f16: the state by the power of two that takes it to below 2^15.
+                int tau = 0;
+                if constexpr (F16) {
+                    top_z = top_of_z();
+                    tau = 141 - top_z;
+                }
+                const float by = F16 ? power2(tau) : 1.f;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     if (SKIP && kk * 32 >= m)
@@ -847,7 +912,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 for (int it = 0; it < IT; ++it) {
                     float w = s.pw[16 * it + oi + 1 - sw.shift] * sw.out_scale;
                     if constexpr (F16)
-                        w = w * power2(rho - tau);
+                        w = w * power2(-tau) * power2(-sigma) * power2(row_scale(s.most[16 * it + oi]));
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         o[it][r] *= w;
@@ -882,10 +947,9 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                         }
                 }
                 if constexpr (F16) {
-                    const float by = power2(-rho);
 #pragma unroll
                     for (int it = 0; it < IT; ++it)
-                        o[it] *= by;
+                        o[it] *= power2(-row_scale(s.most[16 * it + (own & 15)]));
                 }
                 if (sizeof(T) == 2 && sw.out_f32)
                     put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, tok, rev, cnt,
@@ -911,10 +975,13 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
             drift = uniform_double(drift);
             float by = 1.f;
             if constexpr (F16) {
-                int to = 29 - ec - above_exponent(wt_max);
-                to = to < -60 ? -60 : to > 60 ? 60 : to;
-                bound = uniform_float(bound * decay + wt_sum * power2(eb + ec - 28));
-                decay *= power2(to - sigma);
+                // The decayed rows to below 2^15, and the state to below 2^100.
+                if constexpr (STATES)
+                    top_z = top_of_z();
+                int to = 155 - top;
+                to = to < -100 ? -100 : to > 100 ? 100 : to;
+                to = to < sigma + 226 - top_z ? to : sigma + 226 - top_z;
+                decay = decay * power2(to) * power2(-sigma);
                 sigma = to;
                 by = power2(sigma);
             }
@@ -945,10 +1012,16 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                         x[e] *= by;
                 }
                 u32x4 xf[WP];
-                if (bad)
+                if (bad) {
                     parts_of<WP, F16, false>(x, xf);
-                else
+                } else {
+                    // Rows that do not count may be past f16, and meet zeros of b.
+                    if constexpr (F16)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = __builtin_amdgcn_fmed3f(x[e], -32768.f, 32768.f);
                     parts_of<WP, F16, true>(x, xf);
+                }
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     if (SKIP && kk * 32 >= m)
@@ -966,9 +1039,6 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            if constexpr (F16 && !STATES)
-                if (bad)
-                    find_bound();
         }
 
         at = next;
