@@ -471,7 +471,8 @@ typedef struct {
  * out        value_width wide, `heads` heads; overlaps no input.
  * scratch    at least linattn_scratch_bytes(shape) bytes.
  * Nothing at a token that is in no sequence is read; a value that is not
- * finite reaches no earlier token and no other sequence.
+ * finite reaches no earlier token and no other sequence.  Infinities of a
+ * state stay what they are; a sum with a product of one may be NaN instead.
  * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type, widths, heads), ERR_SIZE
  * (more than LIBSCAN_MAX_N tokens or 65535 heads; 2^24 sequences, 2^23 where a
  * width is above 64), ERR_SCRATCH, ERR_HIP.

@@ -148,7 +148,9 @@ __device__ __forceinline__ Power decay_power(float g, double n)
 
 __device__ __forceinline__ float decayed(float x, Power p)
 {
-    return __builtin_fmaf(x, p.hi, x * p.lo);
+    // An infinity times lo, which may be zero or of the other sign, is left out.
+    const float most = 3.402823466e38f;
+    return __builtin_fmaf(x, p.hi, __builtin_amdgcn_fmed3f(x, -most, most) * p.lo);
 }
 
 template <class T>
