@@ -537,9 +537,9 @@ int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const li
  * A row without a token gets token -1, logprob -inf and kept 0.
  *
  * Weights are 64-bit fixed point, 2^(62 - ceil log2 vocab) (2^51 at most) for
- * the largest, rounded to nearest from 64-bit exponentials: their sums are the
- * same in any order.  A weight that rounds to zero counts among the kept, and
- * is never drawn.
+ * the largest.  Each is within 2^-45 of itself, and half a unit, of the
+ * exponential; its sums are exact, and the same in any order.  A weight that
+ * rounds to zero counts among the kept, and is never drawn.
  *
  * logits       device, rows of `vocab` elements, row_stride elements apart.
  * u            device, `rows` floats.

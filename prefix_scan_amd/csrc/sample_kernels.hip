@@ -133,7 +133,8 @@ __device__ __forceinline__ float from_bin(float top, uint32_t bin)
 }
 
 // Weights.  w = 2^y with y = (x - M) log2 e / T is 2^e times entry i of a table
-// of 2^(i / 512) times a cubic of the 2^-10 that are left: 2^-46 off.  The
+// of 2^(i / 512) times a cubic of the 2^-10 that are left.  The cubic is 2^-46
+// off, and so is 1 / T, rounded, times what does not round to zero (y of 52).  The
 // exponent goes into the table's entry, so that one product and sum rounds it
 // to the fixed-point word.  Ten 64-bit operations a weight, which bound a pass
 // over rows without a cut: 512 x 150001 logits take 113 us.
@@ -170,9 +171,10 @@ struct Weigh {
         by = by < most ? by : most;
         least = min_p > 0.f ? (min_p < 1.f ? (double)min_p : 1.0) * one : 0.0;
     }
-    // The weight of a logit, to the nearest fixed-point word (one <= 2^51), and
-    // whether min_p leaves it.  HOW: no min_p, one, or M = +inf; without a
-    // branch, so that several go through at a time.
+    // The weight of a logit, in fixed point (one <= 2^51): 2^-45 of it off, and
+    // half a unit by its rounding to a word; and whether min_p leaves it.  HOW:
+    // no min_p, one, or M = +inf; without a branch, so that several go through
+    // at a time.
     template <int HOW>
     __device__ __forceinline__ uint64_t fixed(float x, bool &in) const
     {
