@@ -684,6 +684,14 @@ def _planned(make, *tensors):
     return plan
 
 
+def _no_gradient(what, *tensors):
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError("%s records no gradient: call it under torch.no_grad(), or linattn and "
+                                   "linattn_grad as the forward and backward of a torch.autograd.Function" % what)
+
+
 def _rows(t, packed):
     """(strides of sequence, token and head, heads) of a [B, T, H, D] tensor's rows, a packed
     [N, H, D] one's or a step's [B, H, D]."""
@@ -811,8 +819,11 @@ def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=Fal
     each shared by consecutive ones); with ends (int32 [B], as
     runs_layout_u32 leaves them) [N, H, D], the sequences one after another.
     state: float32 [B, H, Dk, Dv] before the first token (None: zeros).
-    Returns (out, state_out), state_out None unless want_state or given."""
+    Returns (out, state_out), state_out None unless want_state or given.
+    Neither carries a gradient (linattn_grad has it, for an autograd.Function;
+    examples/recall.py has one): tensors that require one are refused."""
     p = _planned(_linattn_plan, q, k, v, log_decay, ends, state, out, state_out)
+    _no_gradient("linattn", q, k, v, log_decay, state)
     if out is None:
         out = p.new(3)
     if state_out is None and want_state:
@@ -848,6 +859,7 @@ def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dst
     and state_out's dstate_out (None: zeros); dstate is None unless
     want_dstate or given.  Gradients of shared heads are summed."""
     p = _planned(_linattn_grad_plan, dout, q, k, v, log_decay, ends, state, dstate_out, dq, dk, dv, dstate)
+    _no_gradient("linattn_grad", dout, q, k, v, log_decay, state, dstate_out)
     dq, dk, dv = (p.new(i) if t is None else t for i, t in ((4, dq), (5, dk), (6, dv)))
     if dstate is None and want_dstate:
         dstate = p.new_states()
@@ -888,6 +900,7 @@ def linattn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, sta
     if state_out is None:
         state_out = state
     p = _planned(_linattn_step_plan, q, k, v, log_decay, state, slots, out, state_out)
+    _no_gradient("linattn_step", q, k, v, log_decay, state)
     if out is None:
         out = p.new(3)
     _check(lib().linattn_step(p.shape(None, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v),
@@ -923,8 +936,8 @@ def sample_logits(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     one's weight are kept, top_k of them at most, then the fewest whose
     weight is at least top_p; the token is where u of the kept weights, in
     index order, is passed.  temperature 0 is the largest logit.  Returns
-    (tokens int32, logprobs float32, kept int32); a row with nothing but -inf
-    and NaN gets token -1."""
+    (tokens int32, logprobs float32, kept int32), none of them with a gradient;
+    a row with nothing but -inf and NaN gets token -1."""
     each = [t if isinstance(t, torch.Tensor) else None for t in (temperature, top_k, top_p, min_p)]
     code, rows, vocab, stride, device, index, need = _planned(
         _sample_plan, logits, u, *each, tokens, logprobs, kept)
