@@ -414,6 +414,10 @@ int radix_perm_u32(const uint32_t *keys, int32_t *perm, uint64_t n, int bits_per
 /* Element types of the rows (states are always floats). */
 enum { LIBSCAN_F32 = 0, LIBSCAN_BF16 = 1, LIBSCAN_F16 = 2 };
 
+/* Or-ed to the type of linattn and linattn_grad: rows of the outputs at tokens
+ * past a packed batch's last end are zeroed, where otherwise nothing writes. */
+enum { LINATTN_CLEAR_REST = 0x100 };
+
 /* Largest key_width and value_width. */
 #define LINATTN_MAX_WIDTH 128
 
@@ -437,14 +441,14 @@ typedef struct {
  * u32 (what runs_layout_u32 leaves): the sequences lie one after another in
  * `tokens` rows, sequence s at tokens [ends[s - 1], ends[s]); seq_stride is
  * not used.  Ends beyond `tokens` count as `tokens`; outputs of tokens past the
- * last end are not written.  Ends that fall are no batch: what then is in the
+ * last end are not written (but see LINATTN_CLEAR_REST).  Ends that fall are no batch: what then is in the
  * outputs and states is unspecified, and nothing else is read or written.
  * log_decay: device, `heads` floats g, at most 0 in use: what a head's state
  * keeps of itself from token to token is e^g (-inf: no memory).  The decays
  * are constants of the model: there is no gradient for them.
  */
 typedef struct {
-    int dtype;                        /* LIBSCAN_F32 / BF16 / F16, of all rows */
+    int dtype;                        /* LIBSCAN_F32 / BF16 / F16, of all rows; a flag */
     uint32_t seqs, heads, key_width, value_width;
     uint64_t tokens;
     const uint32_t *ends;

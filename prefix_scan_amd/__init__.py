@@ -49,6 +49,7 @@ class LibscanError(RuntimeError):
 
 LINATTN_MAX_WIDTH = 128
 SAMPLE_MAX_VOCAB = 1 << 24
+_CLEAR_REST = 0x100                     # LINATTN_CLEAR_REST
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # LIBSCAN_F32 / BF16 / F16
 
 
@@ -769,11 +770,22 @@ class _Plan:
         self.dtype, self.device, self.index = q.dtype, q.device, q.get_device()
         self.states = (shape.seqs, shape.heads, shape.key_width, shape.value_width)
 
-    def shape(self, ends, log_decay, scale):
-        return _Shape(*self.fields, None if ends is None else ends.data_ptr(), log_decay.data_ptr(), scale)
+    def shape(self, ends, log_decay, scale, clear=False):
+        sh = _Shape(*self.fields, None if ends is None else ends.data_ptr(), log_decay.data_ptr(), scale)
+        if clear:
+            sh.dtype |= _CLEAR_REST
+        return sh
 
-    def new(self, i):
-        return torch.empty(self.rows[i][1], dtype=self.dtype, device=self.device)
+    def new(self, i, zeros=False):
+        return (torch.zeros if zeros else torch.empty)(self.rows[i][1], dtype=self.dtype, device=self.device)
+
+    def new_rows(self, ends, given):
+        """The tensors {index: tensor or None} with new ones for None, and whether the call has to
+        clear their rows past the last end: it does so for all or for none of them."""
+        made = [t is None for t in given.values()]
+        rest = ends is not None and any(made)
+        clear = rest and all(made) and self.fields[1] != 0
+        return [self.new(i, rest and not clear) if t is None else t for i, t in given.items()], clear
 
     def new_states(self):
         return torch.empty(self.states, dtype=torch.float32, device=self.device)
@@ -819,18 +831,19 @@ def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=Fal
     each shared by consecutive ones); with ends (int32 [B], as
     runs_layout_u32 leaves them) [N, H, D], the sequences one after another.
     state: float32 [B, H, Dk, Dv] before the first token (None: zeros).
+    Tokens past the last end are in no sequence: there a given out stays as
+    it is, and a new one holds zeros.
     Returns (out, state_out), state_out None unless want_state or given.
     Neither carries a gradient (linattn_grad has it, for an autograd.Function;
     examples/recall.py has one): tensors that require one are refused."""
     p = _planned(_linattn_plan, q, k, v, log_decay, ends, state, out, state_out)
     _no_gradient("linattn", q, k, v, log_decay, state)
-    if out is None:
-        out = p.new(3)
+    (out,), clear = p.new_rows(ends, {3: out})
     if state_out is None and want_state:
         state_out = p.new_states()
     handle = p.stream(stream)
     with p.scratch(handle, stream) as scr:
-        _check(lib().linattn(p.shape(ends, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v), _addr(state),
+        _check(lib().linattn(p.shape(ends, log_decay, scale, clear), p.at(0, q), p.at(1, k), p.at(2, v), _addr(state),
                              p.at(3, out), _addr(state_out), scr.data_ptr(), scr.numel(), handle), "linattn")
     return out, state_out
 
@@ -857,15 +870,16 @@ def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dst
                  want_dstate=False, dq=None, dk=None, dv=None, dstate=None, stream=None):
     """The gradient of linattn: (dq, dk, dv, dstate) for out's gradient dout
     and state_out's dstate_out (None: zeros); dstate is None unless
-    want_dstate or given.  Gradients of shared heads are summed."""
+    want_dstate or given.  Gradients of shared heads are summed; past the last
+    end they are as linattn's out is."""
     p = _planned(_linattn_grad_plan, dout, q, k, v, log_decay, ends, state, dstate_out, dq, dk, dv, dstate)
     _no_gradient("linattn_grad", dout, q, k, v, log_decay, state, dstate_out)
-    dq, dk, dv = (p.new(i) if t is None else t for i, t in ((4, dq), (5, dk), (6, dv)))
+    (dq, dk, dv), clear = p.new_rows(ends, {4: dq, 5: dk, 6: dv})
     if dstate is None and want_dstate:
         dstate = p.new_states()
     handle = p.stream(stream)
     with p.scratch(handle, stream) as scr:
-        _check(lib().linattn_grad(p.shape(ends, log_decay, scale), p.at(0, dout), p.at(1, q), p.at(2, k),
+        _check(lib().linattn_grad(p.shape(ends, log_decay, scale, clear), p.at(0, dout), p.at(1, q), p.at(2, k),
                                   p.at(3, v), _addr(state), _addr(dstate_out), p.at(4, dq), p.at(5, dk),
                                   p.at(6, dv), _addr(dstate), scr.data_ptr(), scr.numel(), handle),
                "linattn_grad")

@@ -261,6 +261,18 @@ size_t element_bytes(int dtype) { return dtype == LIBSCAN_F32 ? 4 : 2; }
 
 bool bad_type(int dtype) { return dtype < LIBSCAN_F32 || dtype > LIBSCAN_F16; }
 
+// The shape without the flag, which only sequences have, as *clear.
+int take_shape(const linattn_shape_t *s, linattn_shape_t *to, bool *clear)
+{
+    if (!s)
+        return LIBSCAN_ERR_NULL;
+    *to = *s;
+    *clear = s->dtype >= 0 && (s->dtype & LINATTN_CLEAR_REST) != 0;
+    if (*clear)
+        to->dtype &= ~LINATTN_CLEAR_REST;
+    return LIBSCAN_OK;
+}
+
 int check_shape(const linattn_shape_t *s)
 {
     if (!s)
@@ -309,13 +321,14 @@ int widest(const linattn_shape_t &s)
 }
 
 // Everything of a set but its sweeps.
-SweepSet sweep_set(const linattn_shape_t &s, int count)
+SweepSet sweep_set(const linattn_shape_t &s, int count, bool clear = false)
 {
     SweepSet set = {};
     set.count = count;
     set.dtype = s.dtype;
     set.log_decay = s.log_decay;
     set.ends = s.ends;
+    set.clear_from = clear && s.ends ? s.ends + s.seqs - 1 : nullptr;
     set.seqs = s.seqs;
     set.heads = s.heads;
     set.tokens = s.tokens;
@@ -904,19 +917,23 @@ int copy_u32(const uint32_t *src, uint32_t *dst, uint64_t n, void *scratch, size
 
 size_t linattn_scratch_bytes(const linattn_shape_t *shape)
 {
-    if (check_shape(shape) != LIBSCAN_OK || shape->seqs == 0 || too_many_items(*shape, 1))
+    linattn_shape_t sh;
+    bool clear;
+    if (take_shape(shape, &sh, &clear) != LIBSCAN_OK || check_shape(&sh) != LIBSCAN_OK || sh.seqs == 0 ||
+        too_many_items(sh, 1))
         return with_header(0);
-    return with_header(segment_bytes(*shape, 1));
+    return with_header(segment_bytes(sh, 1));
 }
 
 int linattn(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn_rows_t *k,
             const linattn_rows_t *v, const float *state, const linattn_rows_t *out,
             float *state_out, void *scratch, size_t scratch_bytes, hipStream_t stream)
 {
-    int rc = check_shape(shape);
-    if (rc != LIBSCAN_OK)
+    linattn_shape_t sh;
+    bool clear;
+    int rc = take_shape(shape, &sh, &clear);
+    if (rc != LIBSCAN_OK || (rc = check_shape(&sh)) != LIBSCAN_OK)
         return rc;
-    const linattn_shape_t &sh = *shape;
     const bool any = sh.seqs != 0 && sh.tokens != 0;
     if ((rc = check_rows(sh, q, any, false)) != LIBSCAN_OK ||
         (rc = check_rows(sh, k, any, false)) != LIBSCAN_OK ||
@@ -936,7 +953,7 @@ int linattn(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn
     Scratch s;
     if (!carve(scratch, scratch_bytes, segment_bytes(sh, 1), &s))
         return LIBSCAN_ERR_SCRATCH;
-    SweepSet set = sweep_set(sh, 1);
+    SweepSet set = sweep_set(sh, 1, clear);
     set.seg = reinterpret_cast<float *>(s.body());
     Sweep &w = set.s[0];
     w.a = rows_of(sh, *q);
@@ -963,11 +980,13 @@ int linattn(const linattn_shape_t *shape, const linattn_rows_t *q, const linattn
 size_t linattn_grad_scratch_bytes(const linattn_shape_t *shape, uint32_t q_heads, uint32_t k_heads,
                                   uint32_t v_heads)
 {
-    if (check_shape(shape) != LIBSCAN_OK || shape->seqs == 0 || too_many_items(*shape, 3))
+    linattn_shape_t sh;
+    bool clear;
+    if (take_shape(shape, &sh, &clear) != LIBSCAN_OK || check_shape(&sh) != LIBSCAN_OK || sh.seqs == 0 ||
+        too_many_items(sh, 3))
         return with_header(0);
-    return with_header(segment_bytes(*shape, 3) + partial_bytes(*shape, q_heads, shape->key_width) +
-                       partial_bytes(*shape, k_heads, shape->key_width) +
-                       partial_bytes(*shape, v_heads, shape->value_width));
+    return with_header(segment_bytes(sh, 3) + partial_bytes(sh, q_heads, sh.key_width) +
+                       partial_bytes(sh, k_heads, sh.key_width) + partial_bytes(sh, v_heads, sh.value_width));
 }
 
 int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const linattn_rows_t *q,
@@ -976,10 +995,11 @@ int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const
                  const linattn_rows_t *dv, float *dstate, void *scratch, size_t scratch_bytes,
                  hipStream_t stream)
 {
-    int rc = check_shape(shape);
-    if (rc != LIBSCAN_OK)
+    linattn_shape_t sh;
+    bool clear;
+    int rc = take_shape(shape, &sh, &clear);
+    if (rc != LIBSCAN_OK || (rc = check_shape(&sh)) != LIBSCAN_OK)
         return rc;
-    const linattn_shape_t &sh = *shape;
     const bool any = sh.seqs != 0 && sh.tokens != 0;
     if ((rc = check_rows(sh, dout, any, true)) != LIBSCAN_OK)
         return rc;
@@ -1010,7 +1030,7 @@ int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const
     Scratch s;
     if (!carve(scratch, scratch_bytes, at, &s))
         return LIBSCAN_ERR_SCRATCH;
-    SweepSet set = sweep_set(sh, 3);
+    SweepSet set = sweep_set(sh, 3, clear);
     set.seg = reinterpret_cast<float *>(s.body());
     const Rows rq = rows_of(sh, *q), rk = rows_of(sh, *k), rv = rows_of(sh, *v),
                ro = rows_of(sh, *dout);
@@ -1047,6 +1067,7 @@ int linattn_grad(const linattn_shape_t *shape, const linattn_rows_t *dout, const
         h.seqs = sh.ends ? 1 : sh.seqs;
         h.tokens = sh.tokens;
         h.last_end = sh.ends ? sh.ends + sh.seqs - 1 : nullptr;
+        h.clear = clear;
         h.heads = grad[i]->heads;
         h.share = sh.heads / grad[i]->heads;
         h.width = (int)width[i];

@@ -80,6 +80,7 @@ struct SweepSet {
     uint32_t slots;              // states of segments, of each head and sweep
     float *seg;                  // [sweeps][slots][heads] of them
     bool aligned;                // every row starts on 16 bytes and is a whole number of them
+    const uint32_t *clear_from;  // outputs are zeroed from this token on, or null
 };
 
 // Tokens per segment for a set of sweeps (0: no cutting), the number of
@@ -105,6 +106,7 @@ struct HeadSum {
     Rows dst;                    // share unused
     uint64_t tokens, seqs;
     const uint32_t *last_end;    // of a packed batch, or null
+    bool clear;                  // zeros in the rows after it
     uint32_t heads, share;
     int width, dtype;
 };

@@ -57,12 +57,13 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
     const uint64_t all = h.seqs * h.tokens * per;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (uint64_t)gridDim.x * 256) {
         const uint64_t row = i / per, head = i % per / h.width;
-        if (h.last_end && row >= *h.last_end)
+        const bool outside = h.last_end && row >= *h.last_end;
+        if (outside && !h.clear)
             return;
         const int c = (int)(i % h.width);
         const float *src = h.src + (row * h.heads + head) * h.share * h.width + c;
         float x = 0.f;
-        for (uint32_t k = 0; k < h.share; ++k)
+        for (uint32_t k = 0; k < h.share && !outside; ++k)
             x += src[(uint64_t)k * h.width];
         T *dst = static_cast<T *>(const_cast<void *>(h.dst.p));
         dst[(int64_t)(row / h.tokens) * h.dst.seq + (int64_t)(row % h.tokens) * h.dst.tok +

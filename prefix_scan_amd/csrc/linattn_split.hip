@@ -307,7 +307,9 @@ template <class T, bool PERMUTED, int W, int THREADS, int N, int CH, int LD>
 __device__ __forceinline__ void stage(const Unit<T> (&r)[N], uint16_t (*dst)[CH][LD])
 {
     constexpr int PER = W / 8, RS = THREADS / PER;
-    const int tid = afresh((int)threadIdx.x), row0 = tid / PER, unit = tid % PER;
+    // f32 rows leave registers for the addresses.
+    const int tid = sizeof(T) == 4 ? (int)threadIdx.x : afresh((int)threadIdx.x);
+    const int row0 = tid / PER, unit = tid % PER;
     const int col = PERMUTED ? unit / 4 * 32 + (unit & 1) * 16 + (unit & 2) * 2 : unit * 8;
     const auto put = [&](int part, int row, u32x4 w) {
         uint16_t *p = &dst[part][row][col];
@@ -608,9 +610,20 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         head = uniform((uint32_t)(b % set.heads));
     }
     const Sweep &sw = set.s[sweep];
+    // Rows past the last end: each item has some of them; mostly there are none.
+    const auto clear_rest = [&]() {
+        if (STATES || !set.clear_from || sw.out_f32)
+            return;
+        T *const out = static_cast<T *>(sw.out) + (int64_t)head * sw.out_head;
+        for (uint64_t t = *set.clear_from + (uint64_t)item; t < set.tokens; t += gridDim.x)
+            if ((int)threadIdx.x < sw.n)
+                out[(int64_t)t * sw.out_tok + threadIdx.x] = (T)0.f;
+    };
     Place pl;
-    if (!place_of(set, item, STATES, &pl))
+    if (!place_of(set, item, STATES, &pl)) {
+        clear_rest();
         return;
+    }
     pl.seq = uniform(pl.seq);
     pl.first = uniform64(pl.first);
     pl.len = uniform64(pl.len);
@@ -820,8 +833,11 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 }
                 const int d0 = 16 * (it - jt) + oi - 4 * og;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[e] = d0 - e < 0 ? 0.f : acc[e] * s.pair[16 + d0 - e];
+                for (int e = 0; e < 4; ++e) {
+                    acc[e] *= s.pair[16 + d0 - e];
+                    if (d0 - e < 0)
+                        acc[e] = 0.f;
+                }
                 return acc;
             };
             // This lane's four of a tile, in each part.
@@ -1045,6 +1061,7 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         cnt = next_cnt;
     }
 
+    clear_rest();
     if (!active)
         return;
     if constexpr (F16) {
