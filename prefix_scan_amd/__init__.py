@@ -759,6 +759,15 @@ def _out_like(out, name, want, dtype, device):
     return out
 
 
+def _new(shape, dtype, device, stream, zeros=False):
+    """A tensor of the memory of the stream that will write it (None: the current one)."""
+    make = torch.zeros if zeros else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 class _Plan:
     """What a call's layout comes to: the _Shape's fields, and for each tensor of rows its
     strides and the shape that a new one would have."""
@@ -776,19 +785,19 @@ class _Plan:
             sh.dtype |= _CLEAR_REST
         return sh
 
-    def new(self, i, zeros=False):
-        return (torch.zeros if zeros else torch.empty)(self.rows[i][1], dtype=self.dtype, device=self.device)
+    def new(self, i, stream, zeros=False):
+        return _new(self.rows[i][1], self.dtype, self.device, stream, zeros)
 
-    def new_rows(self, ends, given):
+    def new_rows(self, ends, given, stream):
         """The tensors {index: tensor or None} with new ones for None, and whether the call has to
         clear their rows past the last end: it does so for all or for none of them."""
         made = [t is None for t in given.values()]
         rest = ends is not None and any(made)
         clear = rest and all(made) and self.fields[1] != 0
-        return [self.new(i, rest and not clear) if t is None else t for i, t in given.items()], clear
+        return [self.new(i, stream, rest and not clear) if t is None else t for i, t in given.items()], clear
 
-    def new_states(self):
-        return torch.empty(self.states, dtype=torch.float32, device=self.device)
+    def new_states(self, stream):
+        return _new(self.states, torch.float32, self.device, stream)
 
     def stream(self, stream):
         return _raw_stream(self.index) if stream is None else stream.cuda_stream
@@ -838,9 +847,9 @@ def linattn(q, k, v, log_decay, scale=1.0, ends=None, state=None, want_state=Fal
     examples/recall.py has one): tensors that require one are refused."""
     p = _planned(_linattn_plan, q, k, v, log_decay, ends, state, out, state_out)
     _no_gradient("linattn", q, k, v, log_decay, state)
-    (out,), clear = p.new_rows(ends, {3: out})
+    (out,), clear = p.new_rows(ends, {3: out}, stream)
     if state_out is None and want_state:
-        state_out = p.new_states()
+        state_out = p.new_states(stream)
     handle = p.stream(stream)
     with p.scratch(handle, stream) as scr:
         _check(lib().linattn(p.shape(ends, log_decay, scale, clear), p.at(0, q), p.at(1, k), p.at(2, v), _addr(state),
@@ -874,9 +883,9 @@ def linattn_grad(dout, q, k, v, log_decay, scale=1.0, ends=None, state=None, dst
     end they are as linattn's out is."""
     p = _planned(_linattn_grad_plan, dout, q, k, v, log_decay, ends, state, dstate_out, dq, dk, dv, dstate)
     _no_gradient("linattn_grad", dout, q, k, v, log_decay, state, dstate_out)
-    (dq, dk, dv), clear = p.new_rows(ends, {4: dq, 5: dk, 6: dv})
+    (dq, dk, dv), clear = p.new_rows(ends, {4: dq, 5: dk, 6: dv}, stream)
     if dstate is None and want_dstate:
-        dstate = p.new_states()
+        dstate = p.new_states(stream)
     handle = p.stream(stream)
     with p.scratch(handle, stream) as scr:
         _check(lib().linattn_grad(p.shape(ends, log_decay, scale, clear), p.at(0, dout), p.at(1, q), p.at(2, k),
@@ -916,7 +925,7 @@ def linattn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, sta
     p = _planned(_linattn_step_plan, q, k, v, log_decay, state, slots, out, state_out)
     _no_gradient("linattn_step", q, k, v, log_decay, state)
     if out is None:
-        out = p.new(3)
+        out = p.new(3, stream)
     _check(lib().linattn_step(p.shape(None, log_decay, scale), p.at(0, q), p.at(1, k), p.at(2, v),
                               state.data_ptr(), state.shape[0], _addr(slots), p.at(3, out),
                               state_out.data_ptr(), p.stream(stream)), "linattn_step")
@@ -956,11 +965,11 @@ def sample_logits(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     code, rows, vocab, stride, device, index, need = _planned(
         _sample_plan, logits, u, *each, tokens, logprobs, kept)
     if tokens is None:
-        tokens = torch.empty(rows, dtype=torch.int32, device=device)
+        tokens = _new(rows, torch.int32, device, stream)
     if logprobs is None:
-        logprobs = torch.empty(rows, dtype=torch.float32, device=device)
+        logprobs = _new(rows, torch.float32, device, stream)
     if kept is None:
-        kept = torch.empty(rows, dtype=torch.int32, device=device)
+        kept = _new(rows, torch.int32, device, stream)
     a = _Sample(code, rows, vocab, logits.data_ptr(), stride, u.data_ptr(),
                 1.0 if each[0] is not None else temperature,
                 1.0 if each[2] is not None else top_p,
