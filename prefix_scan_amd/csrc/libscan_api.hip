@@ -351,8 +351,7 @@ bool past_a_grid(uint64_t groups, unsigned threads) { return groups * threads > 
 
 bool too_many_items(const linattn_shape_t &s, int count)
 {
-    const uint64_t l = linattn_seg_len(s.tokens, s.ends != nullptr, s.seqs, s.heads, count, widest(s));
-    return past_a_grid(linattn_items(s.tokens, s.ends != nullptr, s.seqs, l), widest(s) <= 64 ? 256 : 512);
+    return past_a_grid(sweep_set(s, count).items, widest(s) <= 64 ? 256 : 512);
 }
 
 uint64_t all_rows(const linattn_shape_t &s) { return s.ends ? s.tokens : s.tokens * s.seqs; }

@@ -197,18 +197,27 @@ size_t linattn_state_floats(int width) { return width <= 64 ? 64 * 64 : 128 * 12
 uint64_t linattn_seg_len(uint64_t tokens, bool ragged, uint32_t seqs, uint32_t heads, int sweeps,
                          int width)
 {
-    // One workgroup for every place on the GPU, and no more: two of 128
-    // columns a compute unit, four of 64.  4 x 32 sequences and heads of 4096
-    // tokens take 239, 202, 236 and 242 us in 2, 4, 6 and 8 segments each
-    // (256, 512, 768 and 1024 workgroups); 16 heads of 65537 take 679, 456,
-    // 529 and 552 us in segments of 4096, 2048, 1408 and 1024.  Segments of
-    // under 256 tokens would move more of states than of rows.
+    // About one workgroup for every place on the GPU.  Those of 128 columns
+    // have two a compute unit, f32's one (93 KB of LDS); those of 64 have
+    // three, f32's two, and take as long with four.  For 256, 512, 768 and
+    // 1024 workgroups, in us:
+    //   bf16 of 128  4 x 4096 x 16  134 119 144 140    gradient of 8192 x 8  113 104 110 110
+    //   f16  of 128                 180 153 184 169                          149 133 135 134
+    //   f32  of 128  4 x 2048 x 16  161 168 168 164                  4096    133 148 147 147
+    //   bf16 of 64                   92  66  67  67                           78  60  53  52
+    //   f16  of 64                  126  87  84  85                          108  79  66  65
+    //   f32  of 64                   95  72  71  71                           90  69  68  68
+    // f32's of 128 are counted as the others: 256 would take 215 for 174 in
+    // gradients of five packed documents, 12 heads, whose lengths differ.
+    // Segments of under 256 tokens would move more of states than of rows.
     const uint64_t places = width <= 64 ? 1024 : 512, lines = (uint64_t)heads * sweeps;
     if (ragged) {
         uint64_t share = (tokens * lines + places - 1) / places;
         // Enough sequences as they are: only what is far longer than its
-        // share is cut (37 of 480 tokens each on average, 24 heads: 222 us
-        // whole, 262 us in shares).
+        // share is cut.  In shares, in three and never, in us: 37 prompts of
+        // 600 tokens on average, 24 heads, f16: 297, 258, 252; 200 of 400,
+        // 8 heads of 64: 148, 134, 131; 40 of 2000, 16 heads: 478, 456, 448;
+        // one of 12000 among 140 of 200, 16 heads: 364, 569, 968.
         if (seqs * lines >= places)
             share *= 3;
         share = (share + 63) / 64 * 64;
