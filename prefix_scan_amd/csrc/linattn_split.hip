@@ -1028,7 +1028,8 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                         x[e] *= by;
                 }
                 u32x4 xf[WP];
-                if (bad) {
+                // f16: powers past 2^98, or not finite, are not scaled down.
+                if (bad || (F16 && top >= 255)) {
                     parts_of<WP, F16, false>(x, xf);
                 } else {
                     // Rows that do not count may be past f16, and meet zeros of b.

@@ -76,3 +76,14 @@ def test_single_tokens_keep_them(widths, dtype):
     with np.errstate(invalid="ignore"):
         wout, wnew = ref.forward(*[host(x[n]) for n in "qkv"], x["g"].numpy(), SCALE, (1,) * 5, host(state))
     assert same(new, wnew) and same(out, wout)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("scale", [INF, float("nan")])
+def test_a_scale_that_is_not_finite_is_seen(scale, dtype):
+    x = make((70,), 2, 2, 2, 16, 16, dtype, 103, state=False)
+    args = [x[n].cuda() for n in ("do", "q", "k", "v")] + [torch.tensor([-0.013, 0.0]).cuda()]
+    out, _ = ps.linattn(*args[1:], scale, x["ends"].cuda())
+    grads = ps.linattn_grad(*args, scale, x["ends"].cuda(), want_dstate=True)
+    for t in (out, *grads):
+        assert not torch.isfinite(t).any()
