@@ -371,10 +371,7 @@ void out_of(const linattn_shape_t &s, Sweep &w, const linattn_rows_t &r, float *
     w.out_head = w.out_f32 ? (int64_t)width : r.head_stride;
     w.out_tok = w.out_f32 ? (int64_t)s.heads * width : r.token_stride;
     w.out_seq = s.ends ? 0 : (w.out_f32 ? (int64_t)s.tokens * s.heads * width : r.seq_stride);
-    const bool whole =
-        w.out_f32 ? width % 4 == 0 && w.out_tok < (1 << 23) : rows_aligned(s, rows_of(s, r), width);
-    const uint64_t bytes = all_rows(s) * s.heads * width * (w.out_f32 || s.dtype == LIBSCAN_F32 ? 4 : 2);
-    w.out_kind = !whole ? kAnywhere : bytes > (32u << 20) ? kPast : kWhole;
+    w.out_whole = w.out_f32 ? width % 4 == 0 && w.out_tok < (1 << 23) : rows_aligned(s, rows_of(s, r), width);
 }
 
 }  // namespace

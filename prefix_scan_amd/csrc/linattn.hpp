@@ -45,14 +45,6 @@ struct Rows {
     uint32_t share;
 };
 
-// How a sweep's outputs are stored: rows that start on 16 bytes and are whole
-// multiples of them, 16 bytes a lane.  kPast: they are more than the L2s hold,
-// and are marked so that they put out nothing that is read again.  134 MB of
-// outputs of 4 x 4096 x 32 x 128: 191 us, 203 unmarked; 1 x 65537 x 16: 432
-// and 431; gradients of 8 x 2048 x 16: 187 to 195, and 197.  10 MB of f32:
-// 173 and 171.
-enum { kAnywhere, kWhole, kPast };
-
 struct Sweep {
     Rows a, b, c;
     void *out;
@@ -60,7 +52,7 @@ struct Sweep {
     int m, n;
     int rev, shift;
     int out_f32;                 // out holds floats (partial gradients of shared heads)
-    int out_kind;
+    int out_whole;               // its rows start on 16 bytes and are whole multiples of them
     float pair_scale, out_scale;
     const float *state_in;       // per (sequence, head) m * n floats, or null
     float *state_out;

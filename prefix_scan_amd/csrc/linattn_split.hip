@@ -14,16 +14,19 @@
 // while chunk t is computed from LDS.  16 columns a wave keep it at 128
 // registers, so that four waves a SIMD hide each other's waits: 4 x 4096
 // tokens of 32 heads of 128 took 166 us with 32 columns a wave and half as
-// many waves, 130 with these (in segments, whose states are another 65).
+// many waves, 130 with these, when bf16's scores and state were one part (and
+// 150 now; in segments, whose states are another 62).  Up to five vector
+// registers and 38 scalar ones are spilled all the same, in the 16-bit kinds
+// of 128.
 //
-// What bounds it.  That sweep moves 590 MB in 130 us, 4.5 TB/s (a copy: 6.8),
-// with 1.3 of 2.4 wave cycles waiting: each wave reads all rows of a and b
+// What bounds it.  That sweep moves 590 MB in 150 us, 3.9 TB/s (a copy: 6.8),
+// with 1.2 of 2.6 wave cycles waiting: each wave reads all rows of a and b
 // from LDS for its 16 columns, 512 bytes for each 16 x 16 x 32 product, and a
 // chunk's memory reads, LDS reads and products follow each other within a
-// workgroup; the two workgroups of a compute unit overlap them in part.  The
-// gradients' sweeps of 8 x 2048 x 16 take 197 us even with no rows read or
-// written; of those, 17 to 52 go with any one of the four steps, and 58 stay
-// without all of them.
+// workgroup; the two workgroups of a compute unit overlap them in part.  With
+// one part, the gradients' sweeps of 8 x 2048 x 16 took 197 us even with no
+// rows read or written; of those, 17 to 52 went with any one of the four
+// steps, and 58 stayed without all of them.
 //
 // How exact.  An operand is one or more 16-bit parts whose products are
 // summed in 32 bits:
@@ -58,18 +61,18 @@
 // column reads of b and c go through 16 rows on end.  Rows of a and of the
 // scores are stored in that order.  Rows of a, b and c are 16 elements longer
 // than they need be, those of the scores trade places by row: no read meets a
-// bank twice.
+// bank twice.  The 8-byte writes of a's rows and of the scores do: two rows of
+// a share their banks, and scores reach half of them (11.9 million cycles of
+// the sweep above, about 20 us of a compute unit's).
 //
 // The chunk is causal by selection, not by multiplication: a masked pair is
-// zero whatever the product was.  A value that is not finite would still
+// zero whatever the product was.  A value of c that is not finite would still
 // reach earlier rows as 0 * inf, so a chunk with one is taken again one token
-// at a time.
+// at a time; those of a and b reach no other row's scores.
 #include "linattn.hpp"
 
 #include "../../include/libscan.h"
 #include "device_common.hpp"
-
-#include <type_traits>
 
 namespace libscan {
 
@@ -502,31 +505,20 @@ __device__ __forceinline__ void hold_rows(OutRows<T, D> &s, const f32x4 *o, int 
 // From there to memory, 16 bytes a lane.
 template <class T, int D, int THREADS>
 __device__ __forceinline__ void put_rows(OutRows<T, D> &s, T *out, int64_t tok, uint64_t at, bool rev, int cnt,
-                                         int n, int kind)
+                                         int n, bool whole)
 {
     constexpr int C = In<T>::kChunk, V = OutRows<T, D>::V, PER = OutRows<T, D>::PIECES, RS = THREADS / PER;
     const int tid = afresh((int)threadIdx.x), row0 = tid / PER, piece = tid % PER, col = piece * V;
-    if (kind != kAnywhere && cnt == C) {
+    if (whole && cnt == C) {
         char *base = reinterpret_cast<char *>(out + (int64_t)(rev ? at - (C - 1) : at) * tok);
         const int64_t step = (rev ? -RS : RS) * tok * (int64_t)sizeof(T);
         const uint32_t place =
             ((uint32_t)(rev ? C - 1 - row0 : row0) * (uint32_t)tok + (uint32_t)col) * (uint32_t)sizeof(T);
         if (col < n) {
-            const auto put = [&](auto past) {
 #pragma unroll
-                for (int k = 0; k < C / RS; ++k) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(s.at(row0 + k * RS, piece));
-                    u32x4 *to = reinterpret_cast<u32x4 *>(base + k * step + place);
-                    if constexpr (past.value)
-                        __builtin_nontemporal_store(w, to);
-                    else
-                        *to = w;
-                }
-            };
-            if (kind == kPast)
-                put(std::true_type{});
-            else
-                put(std::false_type{});
+            for (int k = 0; k < C / RS; ++k)
+                *reinterpret_cast<u32x4 *>(base + k * step + place) =
+                    *reinterpret_cast<const u32x4 *>(s.at(row0 + k * RS, piece));
         }
         return;
     }
@@ -969,14 +961,14 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
                 }
                 if (sizeof(T) == 2 && sw.out_f32)
                     put_out<float, IT>(o, static_cast<float *>(sw.out) + out0, sw.out_tok, tok, rev, cnt,
-                                       wave * 16, n, sw.out_kind);
+                                       wave * 16, n, sw.out_whole);
                 else
                     hold_rows<T, D, IT>(s.outputs(), o, wave, l16, g4);
             }
             if (!(sizeof(T) == 2 && sw.out_f32)) {
                 __syncthreads();
                 put_rows<T, D, THREADS>(s.outputs(), static_cast<T *>(sw.out) + out0, sw.out_tok, tok, rev,
-                                        cnt, n, sw.out_kind);
+                                        cnt, n, sw.out_whole);
             }
         }
         // The state past the chunk.
