@@ -84,7 +84,9 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const HeadSum h)
 // Rows that are no multiple of 16 bytes share their lines and are always kept
 // (484 MiB of 128 x 121: 371 us kept, 638 past).
 // Four rows at a time are as fast as eight or 16 where it is kept (43, 43 and
-// 46 us for 128 MiB), the first four asked for before q and k.
+// 46 us for 128 MiB), the first four asked for before q and k.  Widths of 64
+// leave half of the lanes without columns and move 5.2 to 5.7 TB/s all the
+// same (512 MiB of 128 x 64: 206 us), those of 32 3.7.
 template <class T, int V, int LPR, bool PAST>
 __global__ __launch_bounds__(256) void step_kernel(const StepArgs a)
 {
