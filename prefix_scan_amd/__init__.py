@@ -219,6 +219,15 @@ def _stream_handle(device, stream):
     return ctypes.c_void_p(s.cuda_stream), s
 
 
+def _new(shape, dtype, device, stream, zeros=False):
+    """A tensor of the memory of the stream that will write it (None: the current one)."""
+    make = torch.zeros if zeros else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 # --------------------------------------------------------------------------
 # Scratch: one zero-initialised buffer per (device, stream), grown on demand.
 # The library keeps a buffer consistent between calls by itself, so a buffer
@@ -431,7 +440,7 @@ def runs_layout_u32(counts, ends=None, want_entries=True, entries_dev=None, stre
     _dev_u32(counts, "counts")
     n = counts.numel()
     if ends is None:
-        ends = torch.empty_like(counts)
+        ends = _new(counts.shape, counts.dtype, counts.device, stream)
     _dev_u32(ends, "ends")
     if ends.numel() != n:
         raise ValueError("ends must have as many elements as counts")
@@ -458,7 +467,7 @@ def runs_owner_u32(ends, entry, owner=None, stream=None):
     _dev_u32(ends, "ends")
     _dev_u32(entry, "entry")
     if owner is None:
-        owner = torch.empty(entry.numel(), dtype=torch.int32, device=entry.device)
+        owner = _new(entry.numel(), torch.int32, entry.device, stream)
     _dev_u32(owner, "owner")
     if owner.numel() != entry.numel():
         raise ValueError("owner must have as many elements as entry")
@@ -473,7 +482,7 @@ def runs_owner_all_u32(ends, total, owner=None, stream=None):
     """The owner of every entry 0 .. total-1 (an int32 tensor of `total`)."""
     _dev_u32(ends, "ends")
     if owner is None:
-        owner = torch.empty(total, dtype=torch.int32, device=ends.device)
+        owner = _new(total, torch.int32, ends.device, stream)
     _dev_u32(owner, "owner")
     if owner.numel() != total:
         raise ValueError("owner must have `total` elements")
@@ -497,14 +506,14 @@ def segscan_u32(inp, seg_len, out=None, seg_sums=True, stream=None):
     _dev_u32(inp, "inp")
     n = inp.numel()
     if out is None:
-        out = torch.empty_like(inp)
+        out = _new(inp.shape, inp.dtype, inp.device, stream)
     _dev_u32(out, "out")
     if out.numel() != n:
         raise ValueError("out must have as many elements as inp")
     if seg_len <= 0:
         raise ValueError("seg_len must be positive")
     if seg_sums is True:
-        seg_sums = torch.empty((n + seg_len - 1) // seg_len, dtype=inp.dtype, device=inp.device)
+        seg_sums = _new((n + seg_len - 1) // seg_len, inp.dtype, inp.device, stream)
     if seg_sums is not None:
         _dev_u32(seg_sums, "seg_sums")
         if seg_sums.numel() < (n + seg_len - 1) // seg_len:
@@ -532,13 +541,13 @@ def segscan_flags_u32(inp, flags, out=None, seg_sums=True, want_nsegs=True, nseg
     if flags.numel() != n:
         raise ValueError("flags must have as many elements as inp")
     if out is None:
-        out = torch.empty_like(inp)
+        out = _new(inp.shape, inp.dtype, inp.device, stream)
     _dev_u32(out, "out")
     if out.numel() != n:
         raise ValueError("out must have as many elements as inp")
     made = seg_sums is True
     if made:
-        seg_sums = torch.empty(max(n, 1), dtype=inp.dtype, device=inp.device)
+        seg_sums = _new(max(n, 1), inp.dtype, inp.device, stream)
     if seg_sums is not None:
         _dev_u32(seg_sums, "seg_sums")
     sh, s = _stream_handle(inp.device, stream)
@@ -563,7 +572,7 @@ def compact_flags_u32(flags, out=None, want_count=True, count_dev=None, stream=N
     _dev_u32(flags, "flags")
     n = flags.numel()
     if out is None:
-        out = torch.empty(n, dtype=torch.int32, device=flags.device)
+        out = _new(n, torch.int32, flags.device, stream)
     _dev_u32(out, "out")
     if out.numel() != n:
         raise ValueError("out must have as many elements as flags")
@@ -584,7 +593,7 @@ def radix_perm_u32(keys, bits_per_pass=1, perm=None, stream=None):
     _dev_u32(keys, "keys")
     n = keys.numel()
     if perm is None:
-        perm = torch.empty(n, dtype=torch.int32, device=keys.device)
+        perm = _new(n, torch.int32, keys.device, stream)
     _dev_u32(perm, "perm")
     if perm.numel() != n:
         raise ValueError("perm must have as many elements as keys")
@@ -757,15 +766,6 @@ def _out_like(out, name, want, dtype, device):
         if tuple(out.shape) != tuple(want):
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(want), tuple(out.shape)))
     return out
-
-
-def _new(shape, dtype, device, stream, zeros=False):
-    """A tensor of the memory of the stream that will write it (None: the current one)."""
-    make = torch.zeros if zeros else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
 
 
 class _Plan:

@@ -49,3 +49,39 @@ def test_new_tensors_come_from_the_streams_memory(name):
     assert {t.data_ptr() for t in got} <= at
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def word_calls():
+    n = 300007
+    x = torch.randint(0, 9, (n,), dtype=torch.int32, device="cuda")
+    ends = torch.cumsum(x, 0).to(torch.int32)
+    flags = (x == 0).to(torch.int32)
+    return {
+        "runs_layout": lambda s: [ps.runs_layout_u32(x, want_entries=False, stream=s)[0]],
+        "runs_owner": lambda s: [ps.runs_owner_u32(ends, x, stream=s)],
+        "runs_owner_all": lambda s: [ps.runs_owner_all_u32(ends, n, stream=s)],
+        "segscan": lambda s: list(ps.segscan_u32(x, 7, stream=s)),
+        "segscan_flags": lambda s: list(ps.segscan_flags_u32(x, flags, stream=s)[:2]),
+        "compact": lambda s: [ps.compact_flags_u32(flags, want_count=False, stream=s)[0]],
+        "radix": lambda s: [ps.radix_perm_u32(x, 4, stream=s)],
+    }
+
+
+@pytest.mark.parametrize("name", ["runs_layout", "runs_owner", "runs_owner_all", "segscan", "segscan_flags",
+                                  "compact", "radix"])
+def test_so_do_those_of_the_primitives(name):
+    call = word_calls()[name]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = [t.clone() for t in call(None)]
+    call(side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        mine = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (300007, 300007)]
+    at = {t.data_ptr() for t in mine}
+    del mine
+    got = call(side)
+    torch.cuda.synchronize()
+    assert got[0].data_ptr() in at
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
