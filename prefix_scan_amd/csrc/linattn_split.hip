@@ -974,10 +974,11 @@ __global__ __launch_bounds__(D * 4, sizeof(T) == 4 && !STATES ? 2 : 4) void swee
         // The state past the chunk.
         if (!SKIP || active) {
             // The state is decayed by floats whose product follows p^(tokens)
-            // itself: the rounding of one is made up for by the next.
+            // itself: the rounding of one is made up for by the next.  Of a
+            // subnormal one, whose reciprocal may be infinite, nothing is left.
             const double exact = whole * drift;
             float decay = (float)exact;
-            drift = decay > 0.f && decay < __builtin_inff()
+            drift = decay >= 0x1p-126f && decay < __builtin_inff()
                         ? 1.0 + (exact - (double)decay) * (double)__builtin_amdgcn_rcpf(decay)
                         : 1.0;
             drift = uniform_double(drift);
