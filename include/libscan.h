@@ -518,6 +518,89 @@ int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const li
                  const linattn_rows_t *out, float *state_out, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Gated recurrence of each channel                                         */
+/* ------------------------------------------------------------------------ */
+
+/* What a gate g says about a, the part of its state that a channel keeps:
+ * a = g, a = e^g or a = 1 / (1 + e^-g).  |a| is at most 1 in use. */
+enum { GATESCAN_DECAY = 0, GATESCAN_LOG = 1, GATESCAN_SIGMOID = 2 };
+
+/* Rows of one tensor: token t of sequence s starts `s * seq_stride + t *
+ * token_stride` ELEMENTS after data; the elements of a row are contiguous.
+ * data is aligned to its element. */
+typedef struct {
+    void *data;
+    int64_t seq_stride, token_stride;
+} gatescan_rows_t;
+
+/* seqs, tokens and ends are as in linattn_shape_t.  clear_rest: rows of the
+ * outputs at tokens past a packed batch's last end are zeroed, where otherwise
+ * nothing writes. */
+typedef struct {
+    int dtype;                        /* LIBSCAN_F32 / BF16 / F16, of all rows */
+    int form;                         /* GATESCAN_* */
+    int blend;                        /* 0: b = x, 1: b = (1 - a) x */
+    int clear_rest;
+    uint32_t seqs;
+    uint64_t tokens, width;
+    const uint32_t *ends;
+} gatescan_shape_t;
+
+/*
+ * The recurrence over the tokens t of each sequence, channel by channel,
+ *     h(t) = a(t) h(t - 1) + b(t),    out(t) = h(t),
+ * with a of the token's gate and b of its x: a prefix scan of (a, b) pairs.
+ * Sums, products and states are held in 32 bits and outputs are rounded once;
+ * the order of all sums is fixed.  a below 2^-126 counts as 0.
+ *
+ * state      device, [seqs][width] floats: h before the first token, or NULL
+ *            for zeros.
+ * state_out  the same shape: h after the last token, or NULL.  An empty
+ *            sequence passes its state through.  May not be `state`.
+ * out        overlaps no input.
+ * scratch    at least gatescan_scratch_bytes(shape, 0) bytes.
+ * Nothing at a token that is in no sequence is read; a value that is not
+ * finite reaches no earlier token, no other channel and no other sequence.  An
+ * infinite h stays infinite while a is not 0.
+ * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type, form, flags, width 0), ERR_SIZE
+ * (2^24 sequences, LIBSCAN_MAX_N tokens or channels, or 2^24 tiles of 128
+ * tokens and 64 channels, 32 for f32), ERR_SCRATCH, ERR_HIP.
+ */
+size_t gatescan_scratch_bytes(const gatescan_shape_t *shape, int grad);
+int gatescan(const gatescan_shape_t *shape, const gatescan_rows_t *gate, const gatescan_rows_t *x,
+             const float *state, const gatescan_rows_t *out, float *state_out, void *scratch,
+             size_t scratch_bytes, hipStream_t stream);
+
+/*
+ * Its gradient.  dout is what out's gradient is, dstate_out (or NULL for
+ * zeros) state_out's; out and state are what the forward call left and had:
+ *     dh(t) = dout(t) + a(t + 1) dh(t + 1)     (dstate_out past the end)
+ *     dx(t) = dh(t), or (1 - a(t)) dh(t)
+ *     da(t) = dh(t) h(t - 1), or dh(t) (h(t - 1) - x(t))
+ * and dgate(t) is da(t) times 1, a(t) or a(t) (1 - a(t)).  h(t - 1) is read from
+ * out, as it was rounded there.  x is read with blend only and may be NULL
+ * without.  dstate (or NULL) is the initial state's gradient.  No output may
+ * overlap an input or another output.  scratch: gatescan_scratch_bytes(shape, 1).
+ */
+int gatescan_grad(const gatescan_shape_t *shape, const gatescan_rows_t *dout,
+                  const gatescan_rows_t *gate, const gatescan_rows_t *x, const gatescan_rows_t *out,
+                  const float *state, const float *dstate_out, const gatescan_rows_t *dgate,
+                  const gatescan_rows_t *dx, float *dstate, void *scratch, size_t scratch_bytes,
+                  hipStream_t stream);
+
+/*
+ * One token of each of `seqs` rows, as linattn_step: row r of a tensor starts
+ * at r * seq_stride, and updates the state in slot slots[r] of a pool of `pool`
+ * states [pool][width], or slot r when slots is NULL.  A row whose slot lies
+ * outside [0, pool) is idle: its output is zeros and it touches no state.  A
+ * slot may be listed once only.  state_out: `state` itself, or a pool that
+ * does not overlap it (slots of no row are left as they are).
+ */
+int gatescan_step(const gatescan_shape_t *shape, const gatescan_rows_t *gate,
+                  const gatescan_rows_t *x, const float *state, uint64_t pool, const int32_t *slots,
+                  const gatescan_rows_t *out, float *state_out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Sampling a token from each row of logits                                 */
 /* ------------------------------------------------------------------------ */
 

@@ -9,8 +9,8 @@ a missing ``libscan.so`` raises.
 PyTorch supplies device memory and streams.  Tensors must be on a CUDA (HIP)
 device, contiguous, with 4-byte elements (torch.int32 or torch.uint32), or
 8-byte elements (torch.int64 or torch.uint64) for the *_u64 entry points.
-Rows of linear attention and of logits are float32, bfloat16 or float16, with
-any strides whose last is 1.
+Rows of linear attention, gated recurrences and logits are float32, bfloat16
+or float16, with any strides whose last is 1.
 """
 import ctypes
 import os
@@ -25,6 +25,7 @@ __all__ = [
     "runs_layout_u32", "runs_slots_i32", "runs_owner_u32", "runs_owner_all_u32",
     "segscan_flags_u32",
     "linattn", "linattn_grad", "linattn_step", "sample_logits",
+    "gatescan", "gatescan_grad", "gatescan_step",
     "segscan_u32", "compact_flags_u32", "radix_perm_u32", "copy_u32", "scan_u32_noalloc",
     "scan_scratch_bytes", "scan_ex_scratch_bytes", "segscan_scratch_bytes",
     "compact_scratch_bytes", "radix_scratch_bytes",
@@ -50,6 +51,7 @@ class LibscanError(RuntimeError):
 LINATTN_MAX_WIDTH = 128
 SAMPLE_MAX_VOCAB = 1 << 24
 _CLEAR_REST = 0x100                     # LINATTN_CLEAR_REST
+_FORMS = {"decay": 0, "log": 1, "sigmoid": 2}       # GATESCAN_*
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # LIBSCAN_F32 / BF16 / F16
 
 
@@ -66,6 +68,19 @@ class _Shape(ctypes.Structure):
                 ("key_width", ctypes.c_uint32), ("value_width", ctypes.c_uint32),
                 ("tokens", ctypes.c_uint64), ("ends", ctypes.c_void_p),
                 ("log_decay", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class _GateRows(ctypes.Structure):
+    """gatescan_rows_t"""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class _GateShape(ctypes.Structure):
+    """gatescan_shape_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("form", ctypes.c_int), ("blend", ctypes.c_int),
+                ("clear_rest", ctypes.c_int), ("seqs", ctypes.c_uint32),
+                ("tokens", ctypes.c_uint64), ("width", ctypes.c_uint64), ("ends", ctypes.c_void_p)]
 
 
 class _Sample(ctypes.Structure):
@@ -173,6 +188,15 @@ def lib():
         L.linattn_grad.restype = i32
         L.linattn_step.argtypes = [shape, rows, rows, rows, vp, u64, vp, rows, vp, vp]
         L.linattn_step.restype = i32
+        gshape, grows = ctypes.POINTER(_GateShape), ctypes.POINTER(_GateRows)
+        L.gatescan_scratch_bytes.argtypes = [gshape, i32]
+        L.gatescan_scratch_bytes.restype = sz
+        L.gatescan.argtypes = [gshape, grows, grows, vp, grows, vp, vp, sz, vp]
+        L.gatescan.restype = i32
+        L.gatescan_grad.argtypes = [gshape] + [grows] * 4 + [vp, vp, grows, grows, vp, vp, sz, vp]
+        L.gatescan_grad.restype = i32
+        L.gatescan_step.argtypes = [gshape, grows, grows, vp, u64, vp, grows, vp, vp]
+        L.gatescan_step.restype = i32
         L.sample_scratch_bytes.argtypes = [u64, u64]
         L.sample_scratch_bytes.restype = sz
         L.sample_logits.argtypes = [ctypes.POINTER(_Sample), vp, sz, vp]
@@ -694,12 +718,13 @@ def _planned(make, *tensors):
     return plan
 
 
-def _no_gradient(what, *tensors):
+def _no_gradient(what, *tensors, pair="linattn"):
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
-                raise RuntimeError("%s records no gradient: call it under torch.no_grad(), or linattn and "
-                                   "linattn_grad as the forward and backward of a torch.autograd.Function" % what)
+                raise RuntimeError("%s records no gradient: call it under torch.no_grad(), or %s and "
+                                   "%s_grad as the forward and backward of a torch.autograd.Function"
+                                   % (what, pair, pair))
 
 
 def _rows(t, packed):
@@ -931,6 +956,197 @@ def linattn_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, sta
                               state_out.data_ptr(), p.stream(stream)), "linattn_step")
     return out, state_out
 
+
+# --------------------------------------------------------------------------
+# Gated recurrence of each channel
+# --------------------------------------------------------------------------
+
+class _GatePlan:
+    """What a call's layout comes to: the _GateShape's fields, and for each tensor of rows its
+    strides."""
+
+    def __init__(self, gate, ends, rows, grad):
+        packed = ends is not None
+        step = grad is None
+        tokens = 1 if step else gate.shape[-2]
+        self.lead = gate.shape[:-1]
+        self.dtype, self.device, self.index = gate.dtype, gate.device, gate.get_device()
+        self.fields = (ends.shape[0] if packed else gate.shape[0], tokens, gate.shape[-1])
+        self.states = (self.fields[0], gate.shape[-1])
+        dense = (0 if packed else tokens * gate.shape[-1], gate.shape[-1])
+        self.rows = [dense if t is None else (0 if packed else t.stride(0), 0 if step else t.stride(-2))
+                     for t in rows]
+        self.shape_of = tuple(gate.shape)
+        self.need = 0
+        if not step:
+            shape = _GateShape(_DTYPES[self.dtype], 0, 0, 0, *self.fields, ends.data_ptr() if packed else None)
+            self.need = lib().gatescan_scratch_bytes(shape, int(grad))
+
+    def shape(self, form, blend, ends=None, clear=False):
+        return _GateShape(_DTYPES[self.dtype], form, int(bool(blend)), int(clear), *self.fields, _addr(ends))
+
+    def new(self, stream, zeros=False):
+        return _new(self.shape_of, self.dtype, self.device, stream, zeros)
+
+    def new_rows(self, ends, given, stream):
+        """The tensors with new ones for None, and whether the call has to clear their rows past
+        the last end: it does so for all or for none of them."""
+        made = [t is None for t in given]
+        rest = ends is not None and any(made)
+        clear = rest and all(made) and self.fields[0] != 0
+        return [self.new(stream, rest and not clear) if t is None else t for t in given], clear
+
+    def new_states(self, stream):
+        return _new(self.states, torch.float32, self.device, stream)
+
+    def stream(self, stream):
+        return _raw_stream(self.index) if stream is None else stream.cuda_stream
+
+    def scratch(self, handle, stream):
+        return _scratch_at(self.device, self.index, handle, stream, self.need)
+
+    def at(self, i, t):
+        return _GateRows(_addr(t), *self.rows[i])
+
+
+def _form(form):
+    if form not in _FORMS:
+        raise ValueError("form must be one of %s, got %r" % (sorted(_FORMS), form))
+    return _FORMS[form]
+
+
+def _given(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+
+
+def _gate_rows(gate, dims, *named):
+    """Checks of a call's rows, all of the gate's shape, type and device."""
+    _dev_rows(gate, "gate", dims=dims)
+    if gate.shape[-1] == 0:
+        raise ValueError("gate must be 1 wide at least")
+    for t, name in named:
+        if t is not None:
+            _dev_rows(t, name, gate.dtype, dims, gate.device)
+            if t.shape != gate.shape:
+                raise ValueError("%s must have gate's shape %s, got %s" % (
+                    name, tuple(gate.shape), tuple(t.shape)))
+
+
+def _gate_ends(gate, ends):
+    if ends is not None:
+        _dev_u32(ends, "ends")
+        if ends.device != gate.device or ends.dim() != 1:
+            raise ValueError("ends must be one number for each sequence, on %s" % gate.device)
+    return gate.shape[0] if ends is None else ends.shape[0]
+
+
+def _gate_states(gate, count, *named):
+    for t, name in named:
+        if t is not None:
+            _dev_dense(t, name, torch.float32, (count, gate.shape[-1]), gate.device)
+
+
+def _gatescan_plan(gate, x, ends, state, out, state_out):
+    _given(x, "x")
+    _gate_rows(gate, 3 if ends is None else 2, (x, "x"), (out, "out"))
+    _gate_states(gate, _gate_ends(gate, ends), (state, "state"), (state_out, "state_out"))
+    return _GatePlan(gate, ends, (gate, x, out), False)
+
+
+def gatescan(gate, x, form="decay", blend=False, ends=None, state=None, want_state=False, out=None,
+             state_out=None, stream=None):
+    """A gated recurrence of each channel, over whole sequences:
+    h(t) = a(t) h(t-1) + b(t), and out = h.
+
+    gate and x are [B, T, D], or with ends (int32 [B], as runs_layout_u32
+    leaves them) [N, D], the sequences one after another.  a is the gate
+    itself, its exponential (form="log") or its sigmoid (form="sigmoid"), at
+    most 1 in size; b is x, or (1 - a) x with blend.  state: float32 [B, D]
+    before the first token (None: zeros).  Tokens past the last end are in no
+    sequence: there a given out stays as it is, and a new one holds zeros.
+    Returns (out, state_out), state_out None unless want_state or given.
+    Neither carries a gradient (gatescan_grad has it, for an
+    autograd.Function): tensors that require one are refused."""
+    form = _form(form)
+    p = _planned(_gatescan_plan, gate, x, ends, state, out, state_out)
+    _no_gradient("gatescan", gate, x, state, pair="gatescan")
+    (out,), clear = p.new_rows(ends, [out], stream)
+    if state_out is None and want_state:
+        state_out = p.new_states(stream)
+    handle = p.stream(stream)
+    with p.scratch(handle, stream) as scr:
+        _check(lib().gatescan(p.shape(form, blend, ends, clear), p.at(0, gate), p.at(1, x), _addr(state),
+                              p.at(2, out), _addr(state_out), scr.data_ptr(), scr.numel(), handle), "gatescan")
+    return out, state_out
+
+
+def _gatescan_grad_plan(dout, gate, x, out, ends, state, dstate_out, dgate, dx, dstate):
+    _gate_rows(gate, 3 if ends is None else 2, (dout, "dout"), (x, "x"), (out, "out"), (dgate, "dgate"), (dx, "dx"))
+    _gate_states(gate, _gate_ends(gate, ends), (state, "state"), (dstate_out, "dstate_out"), (dstate, "dstate"))
+    return _GatePlan(gate, ends, (dout, gate, x, out, dgate, dx), True)
+
+
+def gatescan_grad(dout, gate, x, out, form="decay", blend=False, ends=None, state=None, dstate_out=None,
+                  want_dstate=False, dgate=None, dx=None, dstate=None, stream=None):
+    """The gradient of gatescan: (dgate, dx, dstate) for out's gradient dout
+    and state_out's dstate_out (None: zeros); dstate is None unless want_dstate
+    or given.  out is what gatescan returned: the gates' gradient is taken from
+    it as it is rounded there.  Without blend x is not read and may be None.
+    Past the last end the gradients are as gatescan's out is."""
+    form = _form(form)
+    for t, name in ((dout, "dout"), (out, "out")) + (((x, "x"),) if blend else ()):
+        _given(t, name)
+    p = _planned(_gatescan_grad_plan, dout, gate, x, out, ends, state, dstate_out, dgate, dx, dstate)
+    _no_gradient("gatescan_grad", dout, gate, x, out, state, dstate_out, pair="gatescan")
+    (dgate, dx), clear = p.new_rows(ends, [dgate, dx], stream)
+    if dstate is None and want_dstate:
+        dstate = p.new_states(stream)
+    handle = p.stream(stream)
+    with p.scratch(handle, stream) as scr:
+        _check(lib().gatescan_grad(p.shape(form, blend, ends, clear), p.at(0, dout), p.at(1, gate), p.at(2, x),
+                                   p.at(3, out), _addr(state), _addr(dstate_out), p.at(4, dgate), p.at(5, dx),
+                                   _addr(dstate), scr.data_ptr(), scr.numel(), handle), "gatescan_grad")
+    return dgate, dx, dstate
+
+
+def _gatescan_step_plan(gate, x, state, slots, out, state_out):
+    _given(x, "x")
+    _gate_rows(gate, 2, (x, "x"), (out, "out"))
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise TypeError("state must be a torch.Tensor of [P, D]")
+    pool = state.shape[0]
+    _gate_states(gate, pool, (state, "state"), (state_out, "state_out"))
+    if slots is not None:
+        _dev_dense(slots, "slots", torch.int32, (gate.shape[0],), gate.device)
+    elif pool != gate.shape[0]:
+        raise ValueError("without slots, state must hold one state for each of %d rows, got %d"
+                         % (gate.shape[0], pool))
+    return _GatePlan(gate, None, (gate, x, out), None)
+
+
+def gatescan_step(gate, x, state, form="decay", blend=False, slots=None, out=None, state_out=None, stream=None):
+    """One token of each row of gatescan's recurrence: gate, x [B, D]; row r
+    updates state[slots[r]] (state[r] without slots) of the float32 pool
+    [P, D], in place or into state_out.  A row whose slot is outside the pool,
+    as -1, gives zeros and touches nothing; no slot may be listed twice.
+    Returns (out, the pool that was written)."""
+    form = _form(form)
+    if state_out is None:
+        state_out = state
+    p = _planned(_gatescan_step_plan, gate, x, state, slots, out, state_out)
+    _no_gradient("gatescan_step", gate, x, state, pair="gatescan")
+    if out is None:
+        out = p.new(stream)
+    _check(lib().gatescan_step(p.shape(form, blend), p.at(0, gate), p.at(1, x), state.data_ptr(), state.shape[0],
+                               _addr(slots), p.at(2, out), state_out.data_ptr(), p.stream(stream)),
+           "gatescan_step")
+    return out, state_out
+
+
+# --------------------------------------------------------------------------
+# Sampling
+# --------------------------------------------------------------------------
 
 def _sample_plan(logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, kept):
     _dev_rows(logits, "logits", dims=2)

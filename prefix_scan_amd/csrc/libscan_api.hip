@@ -2,6 +2,7 @@
 // scratch carving, kernel selection, and the optional host read-back of a
 // total or count.  All GPU work is enqueued on the caller's stream.
 #include "../../include/libscan.h"
+#include "gatescan.hpp"
 #include "launch.hpp"
 #include "linattn.hpp"
 #include "sample.hpp"
@@ -372,6 +373,69 @@ void out_of(const linattn_shape_t &s, Sweep &w, const linattn_rows_t &r, float *
     w.out_tok = w.out_f32 ? (int64_t)s.heads * width : r.token_stride;
     w.out_seq = s.ends ? 0 : (w.out_f32 ? (int64_t)s.tokens * s.heads * width : r.seq_stride);
     w.out_whole = w.out_f32 ? width % 4 == 0 && w.out_tok < (1 << 23) : rows_aligned(s, rows_of(s, r), width);
+}
+
+// ---------------------------------------------------------------------------
+// Gated recurrence: checks (gatescan.hpp).
+// ---------------------------------------------------------------------------
+
+int check_gate_shape(const gatescan_shape_t *s)
+{
+    if (!s)
+        return LIBSCAN_ERR_NULL;
+    if (bad_type(s->dtype) || s->form < GATESCAN_DECAY || s->form > GATESCAN_SIGMOID ||
+        (s->blend & ~1) != 0 || (s->clear_rest & ~1) != 0 || s->width == 0)
+        return LIBSCAN_ERR_ARG;
+    if (s->seqs > (1u << 24) || s->tokens > LIBSCAN_MAX_N || s->width > LIBSCAN_MAX_N)
+        return LIBSCAN_ERR_SIZE;
+    return misaligned4(s->ends) ? LIBSCAN_ERR_ALIGN : LIBSCAN_OK;
+}
+
+// `any`: the rows hold something (else the tensor's pointer is not looked at).
+int check_gate_rows(const gatescan_shape_t &s, const gatescan_rows_t *r, bool any)
+{
+    if (!r)
+        return LIBSCAN_ERR_NULL;
+    if ((uintptr_t)r->data % element_bytes(s.dtype) != 0)
+        return LIBSCAN_ERR_ALIGN;
+    return any && !r->data ? LIBSCAN_ERR_NULL : LIBSCAN_OK;
+}
+
+GateRows gate_rows_of(const gatescan_shape_t &s, const gatescan_rows_t &r)
+{
+    return GateRows{r.data, s.ends ? 0 : r.seq_stride, r.token_stride};
+}
+
+void gate_out(const gatescan_shape_t &s, const gatescan_rows_t &r, int i, GateArgs *a)
+{
+    a->out[i] = r.data;
+    a->out_seq[i] = s.ends ? 0 : r.seq_stride;
+    a->out_tok[i] = r.token_stride;
+}
+
+// The call's grid and its scratch, prepared.
+int gate_prepare(const gatescan_shape_t &s, bool grad, void *scratch, size_t scratch_bytes, GateArgs *a,
+                 hipStream_t stream)
+{
+    a->dtype = s.dtype;
+    a->form = s.form;
+    a->blend = s.blend != 0;
+    a->clear = s.clear_rest != 0 && s.ends;
+    a->seqs = s.seqs;
+    a->tokens = s.tokens;
+    a->width = s.width;
+    a->ends = s.ends;
+    if (!gate_grid(s.dtype, grad, s.ends != nullptr, s.seqs, s.tokens, s.width, &a->blocks, &a->chains,
+                   &a->tiles))
+        return LIBSCAN_ERR_SIZE;
+    const size_t body = gate_desc_bytes(s.dtype, a->chains, a->tiles);
+    Scratch scr;
+    if (!carve(scratch, scratch_bytes, body, &scr))
+        return LIBSCAN_ERR_SCRATCH;
+    a->ticket = scr.ticket();
+    a->desc = scr.desc();
+    // Lines of one tile use no scratch at all.
+    return body ? hip_status(prepare_state(scr, kKindDesc, 0, body, 1, stream)) : LIBSCAN_OK;
 }
 
 }  // namespace
@@ -1116,6 +1180,125 @@ int linattn_step(const linattn_shape_t *shape, const linattn_rows_t *q, const li
     a.pool = pool;
     a.slots = slots;
     return hip_status(launch_linattn_step(a, stream));
+}
+
+size_t gatescan_scratch_bytes(const gatescan_shape_t *shape, int grad)
+{
+    uint32_t blocks, chains, tiles;
+    if (check_gate_shape(shape) != LIBSCAN_OK || shape->seqs == 0 ||
+        !gate_grid(shape->dtype, grad != 0, shape->ends != nullptr, shape->seqs, shape->tokens, shape->width,
+                   &blocks, &chains, &tiles))
+        return with_header(0);
+    return with_header(gate_desc_bytes(shape->dtype, chains, tiles));
+}
+
+int gatescan(const gatescan_shape_t *shape, const gatescan_rows_t *gate, const gatescan_rows_t *x,
+             const float *state, const gatescan_rows_t *out, float *state_out, void *scratch,
+             size_t scratch_bytes, hipStream_t stream)
+{
+    int rc = check_gate_shape(shape);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    const gatescan_shape_t &s = *shape;
+    const bool any = s.seqs != 0 && s.tokens != 0;
+    if ((rc = check_gate_rows(s, gate, any)) != LIBSCAN_OK || (rc = check_gate_rows(s, x, any)) != LIBSCAN_OK ||
+        (rc = check_gate_rows(s, out, any)) != LIBSCAN_OK)
+        return rc;
+    if (misaligned4(state) || misaligned4(state_out))
+        return LIBSCAN_ERR_ALIGN;
+    if (s.seqs == 0)
+        return LIBSCAN_OK;
+    if (!scratch)
+        return LIBSCAN_ERR_NULL;
+    if (state && state == state_out)
+        return LIBSCAN_ERR_ARG;
+    GateArgs a = {};
+    a.gate = gate_rows_of(s, *gate);
+    a.x = gate_rows_of(s, *x);
+    gate_out(s, *out, 0, &a);
+    a.first = state;
+    a.state_out = state_out;
+    if ((rc = gate_prepare(s, false, scratch, scratch_bytes, &a, stream)) != LIBSCAN_OK)
+        return rc;
+    return hip_status(launch_gatescan(a, stream));
+}
+
+int gatescan_grad(const gatescan_shape_t *shape, const gatescan_rows_t *dout,
+                  const gatescan_rows_t *gate, const gatescan_rows_t *x, const gatescan_rows_t *out,
+                  const float *state, const float *dstate_out, const gatescan_rows_t *dgate,
+                  const gatescan_rows_t *dx, float *dstate, void *scratch, size_t scratch_bytes,
+                  hipStream_t stream)
+{
+    int rc = check_gate_shape(shape);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    const gatescan_shape_t &s = *shape;
+    const bool any = s.seqs != 0 && s.tokens != 0;
+    const gatescan_rows_t *rows[5] = {dout, gate, out, dgate, dx};
+    for (const gatescan_rows_t *r : rows)
+        if ((rc = check_gate_rows(s, r, any)) != LIBSCAN_OK)
+            return rc;
+    if ((x || s.blend) && (rc = check_gate_rows(s, x, any && s.blend)) != LIBSCAN_OK)
+        return rc;
+    if (misaligned4(state) || misaligned4(dstate_out) || misaligned4(dstate))
+        return LIBSCAN_ERR_ALIGN;
+    if (s.seqs == 0)
+        return LIBSCAN_OK;
+    if (!scratch)
+        return LIBSCAN_ERR_NULL;
+    if (dstate && (dstate == state || dstate == dstate_out))
+        return LIBSCAN_ERR_ARG;
+    GateArgs a = {};
+    a.gate = gate_rows_of(s, *gate);
+    if (s.blend)
+        a.x = gate_rows_of(s, *x);
+    a.dout = gate_rows_of(s, *dout);
+    a.h = gate_rows_of(s, *out);
+    gate_out(s, *dgate, 0, &a);
+    gate_out(s, *dx, 1, &a);
+    a.first = state;
+    a.last = dstate_out;
+    a.state_out = dstate;
+    if ((rc = gate_prepare(s, true, scratch, scratch_bytes, &a, stream)) != LIBSCAN_OK)
+        return rc;
+    return hip_status(launch_gatescan_grad(a, stream));
+}
+
+int gatescan_step(const gatescan_shape_t *shape, const gatescan_rows_t *gate,
+                  const gatescan_rows_t *x, const float *state, uint64_t pool, const int32_t *slots,
+                  const gatescan_rows_t *out, float *state_out, hipStream_t stream)
+{
+    int rc = check_gate_shape(shape);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    const gatescan_shape_t &s = *shape;
+    const bool any = s.seqs != 0;
+    if ((rc = check_gate_rows(s, gate, any)) != LIBSCAN_OK || (rc = check_gate_rows(s, x, any)) != LIBSCAN_OK ||
+        (rc = check_gate_rows(s, out, any)) != LIBSCAN_OK)
+        return rc;
+    if (misaligned4(state) || misaligned4(state_out) || misaligned4(slots))
+        return LIBSCAN_ERR_ALIGN;
+    if (!any)
+        return LIBSCAN_OK;
+    if ((!state || !state_out) && pool != 0)
+        return LIBSCAN_ERR_NULL;
+    if (pool > LIBSCAN_MAX_N)
+        return LIBSCAN_ERR_SIZE;
+    GateStepArgs a = {};
+    a.gate = GateRows{gate->data, gate->seq_stride, 0};
+    a.x = GateRows{x->data, x->seq_stride, 0};
+    a.out = out->data;
+    a.out_seq = out->seq_stride;
+    a.dtype = s.dtype;
+    a.form = s.form;
+    a.blend = s.blend != 0;
+    a.rows = s.seqs;
+    a.width = s.width;
+    a.state = state;
+    a.state_out = state_out;
+    a.pool = pool;
+    a.slots = slots;
+    return hip_status(launch_gatescan_step(a, stream));
 }
 
 size_t sample_scratch_bytes(uint64_t rows, uint64_t vocab)
