@@ -601,11 +601,121 @@ int gatescan_step(const gatescan_shape_t *shape, const gatescan_rows_t *gate,
                   const gatescan_rows_t *out, float *state_out, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
-/* Sampling a token from each row of logits                                 */
+/* Rows of a table by their ids (embedding), and the gradient               */
+/* ------------------------------------------------------------------------ */
+
+/* Largest number of rows of a table, and of ids in a call of embed_grad. */
+#define EMBED_MAX_ROWS LIBSCAN_MAX_N_INDEX
+
+typedef struct {
+    int dtype;                        /* LIBSCAN_F32 / BF16 / F16: of weight, or of dout */
+    int out_dtype;                    /* the same: of out, or of dweight */
+    int id_bytes;                     /* 4: int32 ids, 8: int64 ids */
+    uint64_t tokens, rows, width;     /* ids, rows of the table, elements of a row */
+    float scale;
+} embed_shape_t;
+
+/*
+ * out[i] = scale * weight[ids[i]], in 32 bits, rounded once.  An id outside
+ * [0, rows), as -1 for padding, gives zeros.
+ *
+ * ids            device, `tokens` int32 or int64.
+ * weight, out    device; row i starts i * stride ELEMENTS after the pointer,
+ *                which is aligned to its element.  out overlaps no input.
+ * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (types, id_bytes, width 0), ERR_SIZE
+ * (rows above EMBED_MAX_ROWS, tokens or width above LIBSCAN_MAX_N), ERR_HIP.
+ */
+int embed_rows(const embed_shape_t *shape, const void *weight, int64_t weight_stride, const void *ids,
+               void *out, int64_t out_stride, hipStream_t stream);
+
+/*
+ * Its gradient: dweight[v] = scale * (the sum of dout[i] over all i with
+ * ids[i] = v), and zeros in rows of no id; or, with accumulate, that is added
+ * to what dweight holds and rows of no id are left as they are.  Ids outside
+ * [0, rows) are passed over and their rows of dout are not read.  The tokens
+ * are sorted by their rows (stably) and summed in 32 bits in an order that is
+ * the same every time; a row is rounded once.  dweight overlaps no input.
+ * scratch: at least embed_grad_scratch_bytes(shape) bytes.
+ * Errors as above; ERR_SIZE also for more than EMBED_MAX_ROWS tokens;
+ * ERR_ARG for an accumulate other than 0 and 1; ERR_SCRATCH.
+ */
+size_t embed_grad_scratch_bytes(const embed_shape_t *shape);
+int embed_grad(const embed_shape_t *shape, const void *dout, int64_t dout_stride, const void *ids,
+               void *dweight, int64_t dweight_stride, int accumulate, void *scratch,
+               size_t scratch_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Penalties, biases and masks on rows of logits                            */
 /* ------------------------------------------------------------------------ */
 
 /* Largest vocabulary. */
 #define SAMPLE_MAX_VOCAB ((uint64_t)1 << 24)
+
+/* A list of tokens for each row.  ends NULL: `count` a row, row r's at
+ * r * row_stride.  Else device, one u32 a row (what runs_layout_u32 leaves):
+ * row r's are [ends[r - 1], ends[r]) of `count` in all (ends past `count` are
+ * cut to it).  Tokens outside [0, vocab), as -1 for padding, are passed over.
+ * tokens NULL: no list. */
+typedef struct {
+    const int32_t *tokens;
+    int64_t row_stride;
+    uint64_t count;
+    const uint32_t *ends;
+} penalty_list_t;
+
+/*
+ * What sample_logits is given: for each row's logits x, in 32 bits and in this
+ * order, with one rounding at the end,
+ *   a token that is in `past`        x / repetition where x > 0, else x * repetition
+ *   and g times after its prompt     x - (presence + frequency * g) where g > 0
+ *   a token that is in `bias`        x + its value (the last, if it is listed twice)
+ *   a token that the mask bans       -inf
+ * Logits that nothing touches keep their bits.
+ *
+ * repetition <= 0 or NaN, presence NaN, frequency NaN: off.
+ * logits, out   device, rows of `vocab` elements, so many elements apart; out
+ *               is logits itself, with its stride (then only what changes is
+ *               written), or overlaps no input.
+ * prompts       device, `rows` int32: how many of the first of a row's past are
+ *               its prompt, which counts for repetition alone; or NULL: none.
+ * repetitions, presences, frequencies   device, one for each row, or NULL:
+ *               then repetition, presence, frequency hold for all rows.
+ * bias_values   device, floats: one for each token of `bias`, packed as they
+ *               are or bias_stride floats a row.
+ * mask          device, `masks` lists of ceil(vocab / 32) u32, mask_stride
+ *               u32 apart: token t is allowed where bit t % 32 of word t / 32
+ *               is set; or NULL.
+ * mask_slots    device, `rows` int32: the row's mask; outside [0, masks), as
+ *               -1, it has none.  NULL: row r has mask r.
+ * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type; logits in place with another
+ * stride), ERR_SIZE (vocab above SAMPLE_MAX_VOCAB; rows, masks or a list's
+ * count above 2^31 - 1), ERR_HIP.
+ */
+typedef struct {
+    int dtype;                        /* LIBSCAN_F32 / BF16 / F16 */
+    uint64_t rows, vocab;
+    const void *logits;
+    int64_t row_stride;
+    void *out;
+    int64_t out_stride;
+    penalty_list_t past;
+    const int32_t *prompts;
+    float repetition, presence, frequency;
+    const float *repetitions, *presences, *frequencies;
+    penalty_list_t bias;
+    const float *bias_values;
+    int64_t bias_stride;
+    const uint32_t *mask;
+    int64_t mask_stride;
+    uint64_t masks;
+    const int32_t *mask_slots;
+} penalty_args_t;
+
+int penalize_logits(const penalty_args_t *args, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sampling a token from each row of logits                                 */
+/* ------------------------------------------------------------------------ */
 
 /*
  * Per row, with x its logits, M the largest and w(i) = e^((x(i) - M) /

@@ -9,10 +9,11 @@ a missing ``libscan.so`` raises.
 PyTorch supplies device memory and streams.  Tensors must be on a CUDA (HIP)
 device, contiguous, with 4-byte elements (torch.int32 or torch.uint32), or
 8-byte elements (torch.int64 or torch.uint64) for the *_u64 entry points.
-Rows of linear attention, gated recurrences and logits are float32, bfloat16
-or float16, with any strides whose last is 1.
+Rows of linear attention, gated recurrences, embeddings and logits are float32,
+bfloat16 or float16, with any strides whose last is 1.
 """
 import ctypes
+import functools
 import os
 import threading
 
@@ -26,6 +27,7 @@ __all__ = [
     "segscan_flags_u32",
     "linattn", "linattn_grad", "linattn_step", "sample_logits",
     "gatescan", "gatescan_grad", "gatescan_step",
+    "embed_rows", "embed_grad", "penalize_logits",
     "segscan_u32", "compact_flags_u32", "radix_perm_u32", "copy_u32", "scan_u32_noalloc",
     "scan_scratch_bytes", "scan_ex_scratch_bytes", "segscan_scratch_bytes",
     "compact_scratch_bytes", "radix_scratch_bytes",
@@ -50,6 +52,7 @@ class LibscanError(RuntimeError):
 
 LINATTN_MAX_WIDTH = 128
 SAMPLE_MAX_VOCAB = 1 << 24
+EMBED_MAX_ROWS = 0x7FFFFFFF
 _CLEAR_REST = 0x100                     # LINATTN_CLEAR_REST
 _FORMS = {"decay": 0, "log": 1, "sigmoid": 2}       # GATESCAN_*
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # LIBSCAN_F32 / BF16 / F16
@@ -81,6 +84,33 @@ class _GateShape(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int), ("form", ctypes.c_int), ("blend", ctypes.c_int),
                 ("clear_rest", ctypes.c_int), ("seqs", ctypes.c_uint32),
                 ("tokens", ctypes.c_uint64), ("width", ctypes.c_uint64), ("ends", ctypes.c_void_p)]
+
+
+class _Embed(ctypes.Structure):
+    """embed_shape_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("id_bytes", ctypes.c_int),
+                ("tokens", ctypes.c_uint64), ("rows", ctypes.c_uint64), ("width", ctypes.c_uint64),
+                ("scale", ctypes.c_float)]
+
+
+class _List(ctypes.Structure):
+    """penalty_list_t"""
+    _fields_ = [("tokens", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("count", ctypes.c_uint64), ("ends", ctypes.c_void_p)]
+
+
+class _Penalty(ctypes.Structure):
+    """penalty_args_t"""
+    _fields_ = [("dtype", ctypes.c_int), ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64),
+                ("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("past", _List),
+                ("prompts", ctypes.c_void_p), ("repetition", ctypes.c_float),
+                ("presence", ctypes.c_float), ("frequency", ctypes.c_float),
+                ("repetitions", ctypes.c_void_p), ("presences", ctypes.c_void_p),
+                ("frequencies", ctypes.c_void_p), ("bias", _List),
+                ("bias_values", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("masks", ctypes.c_uint64), ("mask_slots", ctypes.c_void_p)]
 
 
 class _Sample(ctypes.Structure):
@@ -197,6 +227,15 @@ def lib():
         L.gatescan_grad.restype = i32
         L.gatescan_step.argtypes = [gshape, grows, grows, vp, u64, vp, grows, vp, vp]
         L.gatescan_step.restype = i32
+        eshape, i64 = ctypes.POINTER(_Embed), ctypes.c_int64
+        L.embed_rows.argtypes = [eshape, vp, i64, vp, vp, i64, vp]
+        L.embed_rows.restype = i32
+        L.embed_grad_scratch_bytes.argtypes = [eshape]
+        L.embed_grad_scratch_bytes.restype = sz
+        L.embed_grad.argtypes = [eshape, vp, i64, vp, vp, i64, i32, vp, sz, vp]
+        L.embed_grad.restype = i32
+        L.penalize_logits.argtypes = [ctypes.POINTER(_Penalty), vp]
+        L.penalize_logits.restype = i32
         L.sample_scratch_bytes.argtypes = [u64, u64]
         L.sample_scratch_bytes.restype = sz
         L.sample_logits.argtypes = [ctypes.POINTER(_Sample), vp, sz, vp]
@@ -718,13 +757,13 @@ def _planned(make, *tensors):
     return plan
 
 
-def _no_gradient(what, *tensors, pair="linattn"):
+def _no_gradient(what, *tensors, pair="linattn", back=None):
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise RuntimeError("%s records no gradient: call it under torch.no_grad(), or %s and "
-                                   "%s_grad as the forward and backward of a torch.autograd.Function"
-                                   % (what, pair, pair))
+                                   "%s as the forward and backward of a torch.autograd.Function"
+                                   % (what, pair, back or pair + "_grad"))
 
 
 def _rows(t, packed):
@@ -1145,8 +1184,229 @@ def gatescan_step(gate, x, state, form="decay", blend=False, slots=None, out=Non
 
 
 # --------------------------------------------------------------------------
-# Sampling
+# Rows of a table by their ids, and the gradient
 # --------------------------------------------------------------------------
+
+def _spaced(t, name):
+    """The stride of t's rows, all of its dimensions but the last taken as one."""
+    stride, count = 0, 1
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if count == 1:
+            stride = s
+        elif s != stride * count:
+            raise ValueError("the rows of %s must be evenly spaced" % name)
+        count *= n
+    return stride
+
+
+def _ids(ids, device):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    if ids.device != device:
+        raise ValueError("ids must be on %s, got %s" % (device, ids.device))
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+
+
+def _embed_plan(rows, to, ids, name):
+    """What _embed_rows_plan and _embed_grad_plan have alike: rows (weight or dout) and ids."""
+    _dev_rows(rows, name)
+    if rows.shape[-1] == 0:
+        raise ValueError("%s must be 1 wide at least" % name)
+    _ids(ids, rows.device)
+    if to not in _DTYPES:
+        raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % to)
+    return (_DTYPES[rows.dtype], _DTYPES[to], ids.element_size(), ids.numel())
+
+
+def _embed_rows_plan(to, weight, ids, out):
+    to = to or (weight.dtype if out is None else out.dtype)
+    fields = _embed_plan(weight, to, ids, "weight")
+    if weight.dim() != 2:
+        raise ValueError("weight must have 2 dimensions, got %d" % weight.dim())
+    want = tuple(ids.shape) + (weight.shape[1],)
+    _out_like(out, "out", want, to, weight.device)
+    return (fields + tuple(weight.shape), weight.stride(0), weight.shape[1] if out is None else _spaced(out, "out"),
+            want, to, weight.device, weight.get_device())
+
+
+def _embed_grad_plan(to, dout, ids, dweight):
+    to = to or (dout.dtype if dweight is None else dweight.dtype)
+    fields = _embed_plan(dout, to, ids, "dout")
+    if dout.shape[:-1] != ids.shape:
+        raise ValueError("dout must have a row for each id, got %s for %s" % (tuple(dout.shape), tuple(ids.shape)))
+    if dweight is not None:
+        _dev_rows(dweight, "dweight", to, 2, dout.device)
+        if dweight.shape[1] != dout.shape[-1]:
+            raise ValueError("dweight must be %d wide, got %d" % (dout.shape[-1], dweight.shape[1]))
+    return (fields, dout.shape[-1], _spaced(dout, "dout"), dout.shape[-1] if dweight is None else dweight.stride(0),
+            to, dout.device, dout.get_device())
+
+
+# By the type asked for, which plans differ by as well.
+_embed_rows_plans = {d: functools.partial(_embed_rows_plan, d) for d in (None, *_DTYPES)}
+_embed_grad_plans = {d: functools.partial(_embed_grad_plan, d) for d in (None, *_DTYPES)}
+
+
+def _embed_type(dtype, plans):
+    if dtype not in plans:
+        raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % (dtype,))
+    return plans[dtype]
+
+
+def embed_rows(weight, ids, scale=1.0, dtype=None, out=None, stream=None):
+    """scale * weight[ids]: rows of the table weight [V, D] by ids (int32 or
+    int64, of any shape), as dtype (None: weight's, or a given out's).  An id
+    outside the table, as -1 for padding, gives zeros.  It carries no
+    gradient (embed_grad has it, for an autograd.Function): a weight that
+    requires one is refused."""
+    fields, stride, out_stride, want, to, device, index = _planned(
+        _embed_type(dtype, _embed_rows_plans), weight, ids, out)
+    _no_gradient("embed_rows", weight, pair="embed_rows", back="embed_grad")
+    if out is None:
+        out = _new(want, to, device, stream)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    _check(lib().embed_rows(_Embed(*fields, scale), weight.data_ptr(), stride, ids.data_ptr(), out.data_ptr(),
+                            out_stride, handle), "embed_rows")
+    return out
+
+
+def embed_grad(dout, ids, rows, scale=1.0, dtype=None, dweight=None, accumulate=False, stream=None):
+    """The gradient of embed_rows for a table of `rows` rows: dweight[v] =
+    scale * the sum of dout[i] over all i with ids[i] = v, as dtype (None:
+    dout's, or a given dweight's), zeros in rows of no id.  With accumulate
+    it is added to the given dweight instead.  The sums' order is the same
+    every time."""
+    fields, width, stride, to_stride, to, device, index = _planned(
+        _embed_type(dtype, _embed_grad_plans), dout, ids, dweight)
+    _no_gradient("embed_grad", dout, pair="embed_rows", back="embed_grad")
+    rows = int(rows)
+    if not 0 <= rows <= EMBED_MAX_ROWS:
+        raise ValueError("rows must be 0 to %d, got %d" % (EMBED_MAX_ROWS, rows))
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dweight to add to")
+        dweight = _new((rows, width), to, device, stream)
+    elif dweight.shape[0] != rows:
+        raise ValueError("dweight must have %d rows, got %d" % (rows, dweight.shape[0]))
+    shape = _Embed(*fields, rows, width, scale)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    with _scratch_at(device, index, handle, stream, lib().embed_grad_scratch_bytes(shape)) as scr:
+        _check(lib().embed_grad(shape, dout.data_ptr(), stride, ids.data_ptr(), dweight.data_ptr(), to_stride,
+                                int(bool(accumulate)), scr.data_ptr(), scr.numel(), handle), "embed_grad")
+    return dweight
+
+
+# --------------------------------------------------------------------------
+# Penalties on logits, and sampling
+# --------------------------------------------------------------------------
+
+def _lists(tokens, ends, name, rows, device):
+    """(stride of a row, elements of a row or in all) of a row's lists, checked."""
+    if tokens is None:
+        if ends is not None:
+            raise ValueError("%s are missing where their ends are given" % name)
+        return 0, 0
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if tokens.dtype != torch.int32:
+        raise TypeError("%s must be int32, got %s" % (name, tokens.dtype))
+    if tokens.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, tokens.device))
+    if ends is not None:
+        _dev_dense(ends, "the ends of %s" % name, (torch.int32, torch.uint32), (rows,), device)
+        _dev_dense(tokens, name, torch.int32, (tokens.numel(),), device)
+        return 0, tokens.numel()
+    if tokens.dim() != 2 or tokens.shape[0] != rows:
+        raise ValueError("%s must be a list for each of %d rows, got %s" % (name, rows, tuple(tokens.shape)))
+    if tokens.shape[1] > 1 and tokens.stride(1) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return tokens.stride(0), tokens.shape[1]
+
+
+def _penalize_plan(logits, tokens, ends, prompt, repetition, presence, frequency, bias_tokens, bias_values,
+                   bias_ends, mask, mask_slots, out):
+    _dev_rows(logits, "logits", dims=2)
+    device, (rows, vocab) = logits.device, logits.shape
+    if vocab > SAMPLE_MAX_VOCAB:
+        raise ValueError("logits must have at most %d columns, got %d" % (SAMPLE_MAX_VOCAB, vocab))
+    _out_like(out, "out", logits.shape, logits.dtype, device)
+    if out is not None and rows > 1 and abs(out.stride(0)) < vocab:
+        raise ValueError("the rows of out overlap")
+    past = _lists(tokens, ends, "tokens", rows, device)
+    bias = _lists(bias_tokens, bias_ends, "bias_tokens", rows, device)
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values come together")
+    values = 0
+    if bias_values is not None:
+        _dev_rows(bias_values, "bias_values", torch.float32, 2 if bias_ends is None else 1, device)
+        if bias_values.shape != bias_tokens.shape:
+            raise ValueError("bias_values must have a value for each of bias_tokens, got %s for %s" % (
+                tuple(bias_values.shape), tuple(bias_tokens.shape)))
+        values = bias_values.stride(0)
+    for t, name, dtype in ((prompt, "prompt", torch.int32), (repetition, "repetition", torch.float32),
+                           (presence, "presence", torch.float32), (frequency, "frequency", torch.float32),
+                           (mask_slots, "mask_slots", torch.int32)):
+        if t is not None:
+            _dev_dense(t, name, dtype, (rows,), device)
+    masks, mask_stride = 0, 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.int32, torch.uint32):
+            raise TypeError("mask must be a torch.Tensor of int32 or uint32 words")
+        if mask.device != device or mask.dim() != 2 or mask.shape[1] != (vocab + 31) // 32:
+            raise ValueError("mask must be [masks, %d] on %s, got %s on %s" % (
+                (vocab + 31) // 32, device, tuple(mask.shape), mask.device))
+        if mask.shape[1] > 1 and mask.stride(1) != 1:
+            raise ValueError("the last dimension of mask must be contiguous")
+        if mask_slots is None and mask.shape[0] != rows:
+            raise ValueError("without mask_slots, mask must have one for each of %d rows, got %d" % (
+                rows, mask.shape[0]))
+        masks, mask_stride = mask.shape[0], mask.stride(0)
+    elif mask_slots is not None:
+        raise ValueError("mask_slots need a mask")
+    return ((_DTYPES[logits.dtype], rows, vocab), logits.stride(0), vocab if out is None else out.stride(0), past,
+            bias, values, mask_stride, masks, logits.dtype, device, logits.get_device())
+
+
+def penalize_logits(logits, tokens=None, ends=None, prompt=None, repetition=1.0, presence=0.0, frequency=0.0,
+                    bias_tokens=None, bias_values=None, bias_ends=None, mask=None, mask_slots=None, out=None,
+                    stream=None):
+    """Logits [R, V] as sample_logits is to have them.  tokens: what each row
+    holds so far, int32 [R, L] (-1 behind shorter ones) or, with ends (int32
+    [R], as runs_layout_u32 leaves them), one row's after another's; the first
+    prompt[r] of a row (int32 [R]; None: none) are its prompt.
+
+    A token among them is divided by repetition where its logit is above 0 and
+    multiplied by it elsewhere; one that came g times after the prompt loses
+    presence + frequency * g; each of these is a number or float32 [R].
+    bias_values (float32) are added to bias_tokens' logits, listed as tokens
+    are (the last value counts where a token is listed twice).  mask: words
+    of 32 bits [G, ceil(V / 32)], a set bit for each token that may follow;
+    row r has mask[mask_slots[r]] (int32 [R], outside as -1: none), mask[r]
+    without slots; what is banned gets -inf.  Returns out, which may be
+    logits itself; it carries no gradient."""
+    each = [t if isinstance(t, torch.Tensor) else None for t in (repetition, presence, frequency)]
+    fields, stride, out_stride, past, bias, values, mask_stride, masks, dtype, device, index = _planned(
+        _penalize_plan, logits, tokens, ends, prompt, *each, bias_tokens, bias_values, bias_ends, mask,
+        mask_slots, out)
+    if torch.is_grad_enabled() and logits.requires_grad:
+        raise RuntimeError("penalize_logits records no gradient: call it under torch.no_grad()")
+    if out is None:
+        out = _new(fields[1:], dtype, device, stream)
+    a = _Penalty(*fields, logits.data_ptr(), stride, out.data_ptr(), out_stride,
+                 _List(_addr(tokens), *past, _addr(ends)), _addr(prompt),
+                 1.0 if each[0] is not None else repetition, 0.0 if each[1] is not None else presence,
+                 0.0 if each[2] is not None else frequency, *map(_addr, each),
+                 _List(_addr(bias_tokens), *bias, _addr(bias_ends)), _addr(bias_values), values,
+                 _addr(mask), mask_stride, masks, _addr(mask_slots))
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    _check(lib().penalize_logits(a, handle), "penalize_logits")
+    return out
+
 
 def _sample_plan(logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, kept):
     _dev_rows(logits, "logits", dims=2)

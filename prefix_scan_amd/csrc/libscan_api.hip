@@ -2,9 +2,11 @@
 // scratch carving, kernel selection, and the optional host read-back of a
 // total or count.  All GPU work is enqueued on the caller's stream.
 #include "../../include/libscan.h"
+#include "embed.hpp"
 #include "gatescan.hpp"
 #include "launch.hpp"
 #include "linattn.hpp"
+#include "penalty.hpp"
 #include "sample.hpp"
 #include "scratch_state.hpp"
 
@@ -373,6 +375,25 @@ void out_of(const linattn_shape_t &s, Sweep &w, const linattn_rows_t &r, float *
     w.out_tok = w.out_f32 ? (int64_t)s.heads * width : r.token_stride;
     w.out_seq = s.ends ? 0 : (w.out_f32 ? (int64_t)s.tokens * s.heads * width : r.seq_stride);
     w.out_whole = w.out_f32 ? width % 4 == 0 && w.out_tok < (1 << 23) : rows_aligned(s, rows_of(s, r), width);
+}
+
+int check_embed(const embed_shape_t *s, const void *table, const void *ids, const void *rows, bool by_row)
+{
+    if (!s)
+        return LIBSCAN_ERR_NULL;
+    if (bad_type(s->dtype) || bad_type(s->out_dtype) || (s->id_bytes != 4 && s->id_bytes != 8) || s->width == 0)
+        return LIBSCAN_ERR_ARG;
+    if (s->rows > EMBED_MAX_ROWS || s->tokens > LIBSCAN_MAX_N || s->width > LIBSCAN_MAX_N ||
+        (by_row && s->tokens > EMBED_MAX_ROWS))
+        return LIBSCAN_ERR_SIZE;
+    // The table is weight or dweight, the rows out or dout.
+    if ((uintptr_t)table % element_bytes(by_row ? s->out_dtype : s->dtype) != 0 ||
+        (uintptr_t)rows % element_bytes(by_row ? s->dtype : s->out_dtype) != 0 ||
+        (uintptr_t)ids % (unsigned)s->id_bytes != 0)
+        return LIBSCAN_ERR_ALIGN;
+    if ((!table && s->rows != 0) || ((!rows || !ids) && s->tokens != 0))
+        return LIBSCAN_ERR_NULL;
+    return LIBSCAN_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -1299,6 +1320,98 @@ int gatescan_step(const gatescan_shape_t *shape, const gatescan_rows_t *gate,
     a.pool = pool;
     a.slots = slots;
     return hip_status(launch_gatescan_step(a, stream));
+}
+
+int embed_rows(const embed_shape_t *shape, const void *weight, int64_t weight_stride, const void *ids,
+               void *out, int64_t out_stride, hipStream_t stream)
+{
+    const int rc = check_embed(shape, weight, ids, out, false);
+    if (rc != LIBSCAN_OK || shape->tokens == 0)
+        return rc;
+    EmbedRowsArgs a = {};
+    a.weight = weight;
+    a.out = out;
+    a.ids = ids;
+    a.weight_stride = weight_stride;
+    a.out_stride = out_stride;
+    a.dtype = shape->dtype;
+    a.out_dtype = shape->out_dtype;
+    a.id_bytes = shape->id_bytes;
+    a.tokens = shape->tokens;
+    a.rows = shape->rows;
+    a.width = shape->width;
+    a.scale = shape->scale;
+    return hip_status(launch_embed_rows(a, stream));
+}
+
+size_t embed_grad_scratch_bytes(const embed_shape_t *shape)
+{
+    if (!shape || shape->tokens > EMBED_MAX_ROWS || shape->rows > EMBED_MAX_ROWS || shape->width > LIBSCAN_MAX_N)
+        return with_header(0);
+    return with_header(embed_grad_body_bytes(shape->tokens, shape->rows, shape->width));
+}
+
+int embed_grad(const embed_shape_t *shape, const void *dout, int64_t dout_stride, const void *ids,
+               void *dweight, int64_t dweight_stride, int accumulate, void *scratch,
+               size_t scratch_bytes, hipStream_t stream)
+{
+    const int rc = check_embed(shape, dweight, ids, dout, true);
+    if (rc != LIBSCAN_OK)
+        return rc;
+    if ((accumulate & ~1) != 0)
+        return LIBSCAN_ERR_ARG;
+    const embed_shape_t &s = *shape;
+    if (s.rows == 0 || (s.tokens == 0 && accumulate))
+        return LIBSCAN_OK;
+    if (!scratch)
+        return LIBSCAN_ERR_NULL;
+    Scratch scr;
+    if (!carve(scratch, scratch_bytes, embed_grad_body_bytes(s.tokens, s.rows, s.width), &scr))
+        return LIBSCAN_ERR_SCRATCH;
+    EmbedGradArgs a = {};
+    a.dout = dout;
+    a.dweight = dweight;
+    a.ids = ids;
+    a.dout_stride = dout_stride;
+    a.dweight_stride = dweight_stride;
+    a.dtype = s.dtype;
+    a.out_dtype = s.out_dtype;
+    a.id_bytes = s.id_bytes;
+    a.tokens = (uint32_t)s.tokens;
+    a.rows = s.rows;
+    a.width = s.width;
+    a.scale = s.scale;
+    a.accumulate = accumulate != 0;
+    hipError_t e = prepare_state(scr, kKindData, 0, 0, 0, stream);
+    if (e == hipSuccess)
+        e = launch_embed_grad(a, scr.body(), stream);
+    return hip_status(e);
+}
+
+int penalize_logits(const penalty_args_t *args, hipStream_t stream)
+{
+    if (!args)
+        return LIBSCAN_ERR_NULL;
+    const penalty_args_t &a = *args;
+    if (bad_type(a.dtype))
+        return LIBSCAN_ERR_ARG;
+    const uint64_t most = LIBSCAN_MAX_N_INDEX;
+    if (a.vocab > SAMPLE_MAX_VOCAB || a.rows > most || a.masks > most || a.past.count > most || a.bias.count > most)
+        return LIBSCAN_ERR_SIZE;
+    if ((uintptr_t)a.logits % element_bytes(a.dtype) != 0 || (uintptr_t)a.out % element_bytes(a.dtype) != 0 ||
+        misaligned4(a.past.tokens) || misaligned4(a.past.ends) || misaligned4(a.prompts) ||
+        misaligned4(a.repetitions) || misaligned4(a.presences) || misaligned4(a.frequencies) ||
+        misaligned4(a.bias.tokens) || misaligned4(a.bias.ends) || misaligned4(a.bias_values) ||
+        misaligned4(a.mask) || misaligned4(a.mask_slots))
+        return LIBSCAN_ERR_ALIGN;
+    if (a.rows == 0 || a.vocab == 0)
+        return LIBSCAN_OK;
+    if (!a.logits || !a.out || (a.past.count != 0 && !a.past.tokens) || (a.bias.count != 0 && !a.bias.tokens) ||
+        (a.bias.tokens && a.bias.count != 0 && !a.bias_values) || (!a.mask && a.masks != 0))
+        return LIBSCAN_ERR_NULL;
+    if (a.logits == a.out && a.row_stride != a.out_stride)
+        return LIBSCAN_ERR_ARG;
+    return hip_status(launch_penalize(a, stream));
 }
 
 size_t sample_scratch_bytes(uint64_t rows, uint64_t vocab)
