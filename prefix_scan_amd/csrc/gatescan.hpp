@@ -27,6 +27,7 @@ namespace libscan {
 
 constexpr int kGateLanes = 8;          // lanes of a row: 16 bytes each
 constexpr int kGateThreads = 256;
+constexpr int kGateWindow = 12;        // tiles that a look back spans at most
 constexpr int kGateGroups = kGateThreads / kGateLanes;
 
 // Tokens of a thread, and of a tile.
@@ -53,12 +54,19 @@ struct GateArgs {
     float *state_out;                  // h after the last token; or the gradient of `first`; or null
     uint32_t blocks;                   // tiles along the width
     uint32_t chains, tiles;            // lines of tiles, and the tiles of each
+    uint32_t adjacent, draws;          // tiles side by side that are drawn at once, and how many draws there are
+    bool far;                          // a look back spans kGateWindow tiles, else four
     uint64_t *ticket, *desc;           // of the chained carry, where there is more than one tile
 };
 
 // Lines of tiles and tiles of each; false where a grid cannot hold them.
 bool gate_grid(int dtype, bool grad, bool packed, uint32_t seqs, uint64_t tokens, uint64_t width,
                uint32_t *blocks, uint32_t *chains, uint32_t *tiles);
+// How many tiles side by side are drawn at once.
+uint32_t gate_adjacent(uint32_t chains, uint32_t tiles);
+// Whether looks back span kGateWindow tiles, not four: a chained value moves so
+// many tiles in the time of a look, about a microsecond.
+bool gate_far(uint32_t chains);
 size_t gate_desc_bytes(int dtype, uint32_t chains, uint32_t tiles);
 
 hipError_t launch_gatescan(const GateArgs &a, hipStream_t stream);

@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void gate_step_kernel(GateStepArgs p)
         load_floats<V>(p.state + slot * p.width + c, n, h);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const Gate w = gate_of<FORM>(U::get(g, e));
+            const Gate w = gate_of<FORM, sizeof(T) == 4>(U::get(g, e));
             const float v = U::get(x, e);
             h[e] = __builtin_fmaf(w.a, h[e], BLEND ? w.rest * v : v);
         }
@@ -72,6 +72,17 @@ bool gate_grid(int dtype, bool grad, bool packed, uint32_t seqs, uint64_t tokens
     *tiles = (uint32_t)k;
     return true;
 }
+
+uint32_t gate_adjacent(uint32_t chains, uint32_t tiles)
+{
+    const uint64_t all = (uint64_t)chains * tiles;
+    uint32_t n = 1;
+    while (n < 4 && n * 2 <= chains && all / (n * 2) >= 1024)
+        n *= 2;
+    return n;
+}
+
+bool gate_far(uint32_t chains) { return chains < 128; }
 
 size_t gate_desc_bytes(int dtype, uint32_t chains, uint32_t tiles)
 {

@@ -1,16 +1,21 @@
 // gatescan_tile.hpp -- the kernel of the gated recurrence and of its gradient
-// (gatescan.hpp has the formulas), on one tile a workgroup.
+// (gatescan.hpp has the formulas).
 //
 // A thread has R tokens, one after another, of 16 bytes of channels; eight
-// lanes share a row, so that each load of a wave is eight whole lines.  The
-// threads scan their tokens, one wave chains the groups of a channel through
-// LDS, takes the carry from the tiles before and hands every group its own,
-// and the threads go over their tokens once more from there.
+// lanes share a row, so that each load of a wave is eight whole lines.  Per
+// tile,
+//   1. the threads scan their tokens and leave a pair for each channel in LDS;
+//   2. one wave, a lane a channel, chains the pairs of the tile's groups, looks
+//      back for what enters the tile and publishes what leaves it;
+//   3. the threads go over their tokens once more from what enters them, and
+//      store.
 //
 // Bound: memory.  Rows are read and written once (descriptors of the carry
-// add 1.5 KB to a tile of 48 KB and more).  Tiles are drawn from a ticket
-// in the order of their place in their lines, all lines' first tiles first: a
-// tile waits only on tiles that were drawn before it.
+// add 1.5 KB to a tile of 48 KB and more).  A workgroup draws a few tiles side
+// by side from a ticket (one word's draws are served 12 ns apart, a tile of
+// 48 KB takes 7), in the order of their place in their lines, all lines' first
+// tiles first: a tile waits only on tiles that were drawn before it, by
+// workgroups that work on theirs in that order.
 #pragma once
 
 #include "device_common.hpp"
@@ -20,40 +25,53 @@
 
 namespace libscan {
 
-// a and 1 - a of a gate.  e^x is 2^(x log2 e) with what that product's rounding
-// left put back (log2 e in two parts), so that it is good to about one step at
-// any x; past 200 of 0 the power has long been 0 or infinite.  Near a = 1 the
-// smaller of a and 1 - a is computed and the other is 1 less it: a state's
-// memory is 1 / (1 - a) tokens long, and each step's error counts that often.
+// a and 1 - a of a gate.  e^x is 2^(x log2 e).  For f32 rows what that
+// product's rounding left is put back (log2 e in two parts), so that it is
+// good to about one step at any x; 16-bit rows are rounded to 2^-9 and 2^-12
+// of themselves, and an error of x 2^-24 in e^x is left in.  Near a = 1 the
+// smaller of a and 1 - a is computed and the other is 1 less it, for all rows:
+// a state's memory is 1 / (1 - a) tokens long, and each step's error counts
+// that often.
+template <bool FINE>
 __device__ __forceinline__ float gate_exp(float x)
 {
-    x = x > 200.f ? 200.f : x;
-    x = x < -200.f ? -200.f : x;
     const float hi = 1.44269502f, lo = 1.92596299e-8f;
-    const float t = x * hi;
+    const float t = x * hi, p = __builtin_amdgcn_exp2f(t);
+    if (!FINE)
+        return p;
+    // rest is below 2^-16: 2^rest = 1 + rest ln 2.  Nothing is put back to 0
+    // and infinity, where rest may be NaN.
     const float rest = __builtin_fmaf(x, lo, __builtin_fmaf(x, hi, -t));
-    const float p = __builtin_amdgcn_exp2f(t);
-    // rest is below 2^-16: 2^rest = 1 + rest ln 2.
-    return __builtin_fmaf(p, p < __builtin_inff() ? rest * 0.693147182f : 0.f, p);
+    return p > 0.f && p < __builtin_inff() ? __builtin_fmaf(p, rest * 0.693147182f, p) : p;
 }
 
 struct Gate {
     float a, rest;       // a, 1 - a
 };
 
-template <int FORM>
+template <int FORM, bool FINE>
 __device__ __forceinline__ Gate gate_of(float g)
 {
     if (FORM == GATESCAN_DECAY)
         return Gate{g, 1.f - g};
     if (FORM == GATESCAN_SIGMOID) {
-        const float e = gate_exp(-__builtin_fabsf(g)), d = 1.f + e;
+        const float e = gate_exp<FINE>(-__builtin_fabsf(g)), d = 1.f + e;
         float r = __builtin_amdgcn_rcpf(d);
-        r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+        if (FINE)
+            r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
         const float small = e * r, large = 1.f - small;
         return g < 0.f ? Gate{small, large} : Gate{large, small};
     }
-    // 1 - e^g from its series near 0 (eight terms: 0.35^8 / 9! is below 2^-30).
+    const float p = gate_exp<FINE>(g);
+    if (!FINE) {
+        // 1 - e^g from its series near 0 (0.1^6 / 6! is below 2^-29).
+        float s = __builtin_fmaf(g, 1.f / 120.f, 1.f / 24.f);
+        s = __builtin_fmaf(s, g, 1.f / 6.f);
+        s = __builtin_fmaf(s, g, 0.5f);
+        s = __builtin_fmaf(s * g, g, g);
+        return __builtin_fabsf(g) < 0.1f ? Gate{1.f + s, -s} : Gate{p, 1.f - p};
+    }
+    // Eight terms: 0.35^8 / 9! is below 2^-30.
     float s = __builtin_fmaf(g, 1.f / 40320.f, 1.f / 5040.f);
     s = __builtin_fmaf(s, g, 1.f / 720.f);
     s = __builtin_fmaf(s, g, 1.f / 120.f);
@@ -61,420 +79,699 @@ __device__ __forceinline__ Gate gate_of(float g)
     s = __builtin_fmaf(s, g, 1.f / 6.f);
     s = __builtin_fmaf(s, g, 0.5f);
     s = __builtin_fmaf(s * g, g, g);
-    const float p = gate_exp(g);
     return __builtin_fabsf(g) < 0.35f ? Gate{1.f + s, -s} : Gate{p, 1.f - p};
 }
 
-// A product of gates that has left the floats counts as the smallest of them,
-// not as zero, unless one of its factors is zero: an infinite state stays one.
-__device__ __forceinline__ float kept_product(float A, bool zero)
+// The product of two products of gates.  One that has left the floats counts
+// as the smallest of them, not as zero, unless a factor is zero: an infinite
+// state stays infinite.
+template <bool SIGNED>
+__device__ __forceinline__ float kept_product(float a, float b)
 {
-    return A == 0.f && !zero ? __builtin_copysignf(1.40129846e-45f, A) : A;
+    const float least = __builtin_fminf(__builtin_fminf(__builtin_fabsf(a), __builtin_fabsf(b)), 1.40129846e-45f);
+    const float p = a * b, q = __builtin_fmaxf(__builtin_fabsf(p), least);
+    return SIGNED ? __builtin_copysignf(q, p) : q;
 }
 
 template <class T, int FORM, bool BLEND, bool GRAD>
-__global__ __launch_bounds__(kGateThreads, 4) void gatescan_kernel(GateArgs p)
-{
+struct GateTile {
     typedef Unpack<T> U;
-    constexpr int V = kPiece<T>, C = kGateLanes * V, G = kGateGroups;
-    constexpr int R = gate_rows(sizeof(T) == 4 ? LIBSCAN_F32 : LIBSCAN_BF16, GRAD), TT = G * R;
-    static_assert(C <= 64 && G <= C, "one wave chains the groups");
-    __shared__ __align__(16) float s_a[G][C], s_h[G][C];
-    __shared__ uint32_t s_reset[G];
-    __shared__ int32_t s_first[TT], s_last[TT];     // the sequence that starts / ends at a token, or -1
-    __shared__ uint32_t s_ticket[2], s_seq;
+    static constexpr int V = kPiece<T>, C = kGateLanes * V, G = kGateGroups;
+    static constexpr int R = gate_rows(sizeof(T) == 4 ? LIBSCAN_F32 : LIBSCAN_BF16, GRAD), TT = G * R;
+    static constexpr bool FINE = sizeof(T) == 4;
+    // Of any tile: a thread has four channels of some tokens.
+    static constexpr int kParts = kGateThreads * 4 / C, kTokens = TT / kParts;
+    static_assert(C <= 64 && kParts <= G && G <= 32 && G % 8 == 0 && kParts % 8 == 0, "one wave chains the groups");
 
-    const int tid = threadIdx.x, lane8 = tid % kGateLanes, group = tid / kGateLanes;
-    const bool chained = p.tiles > 1;
-    uint32_t at = blockIdx.x, tag = 0;
-    if (chained) {
-        if (tid == 0) {
-            const TileTicket t = draw_ticket(p.ticket, p.chains * p.tiles);
-            s_ticket[0] = t.tile;
-            s_ticket[1] = t.tag;
-        }
-        __syncthreads();
-        at = __builtin_amdgcn_readfirstlane(s_ticket[0]);
-        tag = __builtin_amdgcn_readfirstlane(s_ticket[1]);
-    }
-    const uint32_t k = at / p.chains, chain = at % p.chains;
-    const uint32_t seq = chain / p.blocks;
-    const uint64_t c0 = (uint64_t)(chain % p.blocks) * C + lane8 * V;
-    const int n = c0 < p.width ? (int)(p.width - c0 < (uint64_t)V ? p.width - c0 : V) : 0;
+    static constexpr int kStash = GRAD ? 2 * R : R * V / 2;      // pieces that a thread keeps
 
-    // Tokens [0, end) are in sequences; the tile has places [k TT, k TT + TT) in
-    // the sweep's order, the thread R from `place` on.
-    uint64_t end = p.tokens;
-    if (p.ends) {
-        const uint64_t last = p.ends[p.seqs - 1];
-        end = last < end ? last : end;
-    }
-    const uint64_t tile0 = (uint64_t)k * TT;
-    const uint64_t place = tile0 + (uint64_t)group * R;
-    const auto token = [&](int r) -> int64_t {
-        const int64_t x = (int64_t)(place + r);
-        return GRAD ? (int64_t)p.tokens - 1 - x : x;
-    };
-    const auto inside = [&](int r) { const int64_t t = token(r); return t >= 0 && t < (int64_t)end; };
-    const auto row = [&](const GateRows &s, int64_t t) {
-        return static_cast<const T *>(s.p) + (int64_t)seq * s.seq + t * s.tok + c0;
+    struct Shared {
+        // Each group's pair, then that of all groups before it in the tile.
+        alignas(16) float a[G][C];
+        alignas(16) float h[G][C];
+        alignas(16) float carry[C];                  // what enters the tile
+        piece_t kept[kStash][64];
+        uint32_t reset[kParts];                      // whether the sweep starts anew in a part
+        uint32_t draw, tag, seq;
+        int32_t first[TT], last[TT];                 // the sequence that starts / ends at a token, or -1
     };
 
-    // All of the thread's rows are asked for at once.
-    const bool whole = inside(0) && inside(R - 1);
-    piece_t rg[R], rx[R], rd[R], rh[R];
-    const piece_t none = {0, 0, 0, 0};
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rg[r] = rx[r] = rd[r] = rh[r] = none;
-        if (n > 0 && (whole || inside(r))) {
-            const int64_t t = token(r);
-            rg[r] = load_piece<T>(row(p.gate, t), n);
-            if (!GRAD || BLEND)
-                rx[r] = load_piece<T>(row(p.x, t), n);
-            if (GRAD) {
-                rd[r] = load_piece<T>(row(p.dout, t), n);
-                if (t > 0)
-                    rh[r] = load_piece<T>(row(p.h, t - 1), n);
-            }
+    // The call's arguments, in the kernel's own memory.
+    typedef const __attribute__((address_space(4))) GateArgs Args;
+
+    Args *p;
+    Shared &s;
+    uint64_t end;                // tokens [0, end) are in sequences
+    uint32_t k, chain, count;    // the workgroup's tiles: `count` lines from `chain` on
+    int64_t low;                 // their lowest token (below 0 where a gradient's last tile reaches past them)
+
+    __device__ __forceinline__ GateTile(Shared &shared, uint32_t number) : s(shared)
+    {
+        p = (Args *)__builtin_amdgcn_kernarg_segment_ptr();
+        end = p->tokens;
+        if (p->ends) {
+            const uint64_t last = p->ends[p->seqs - 1];
+            end = last < end ? last : end;
         }
+        const uint32_t lines = (p->chains + p->adjacent - 1) / p->adjacent;
+        k = number / lines;
+        chain = number % lines * p->adjacent;
+        count = p->chains - chain < p->adjacent ? p->chains - chain : p->adjacent;
+        low = GRAD ? (int64_t)p->tokens - (int64_t)(k + 1) * TT : (int64_t)k * TT;
     }
 
-    // Where sequences start and end among the tile's tokens.
-    uint32_t firsts = 0, lasts = 0;      // the thread's, a bit a token
-    const int64_t tok0 = GRAD ? (int64_t)p.tokens - (int64_t)(tile0 + TT) : (int64_t)tile0;   // lowest token
-    if (p.ends) {
+    // The token at one of the tile's places in the sweep's order.
+    __device__ __forceinline__ int64_t token(int at) const { return GRAD ? low + (TT - 1 - at) : low + at; }
+
+    // Where a line's channels start, and how many of them a thread has that
+    // starts `at` into them.
+    __device__ __forceinline__ uint64_t column(uint32_t line) const { return (uint64_t)(line % p->blocks) * C; }
+
+    template <class Rows>
+    __device__ __forceinline__ const T *row(const Rows &from, uint32_t line, int64_t t) const
+    {
+        return static_cast<const T *>(from.p) + (int64_t)(line / p->blocks) * from.seq + t * from.tok +
+               (int64_t)column(line);
+    }
+    __device__ __forceinline__ T *out_row(int which, uint32_t line, int64_t t) const
+    {
+        return static_cast<T *>(p->out[which]) + (int64_t)(line / p->blocks) * p->out_seq[which] +
+               t * p->out_tok[which] + (int64_t)column(line);
+    }
+
+    // Where sequences start and end among the tile's tokens, and whether any
+    // does; the states of empty ones are passed through, in the workgroup's
+    // channels, by the tiles at whose tokens they lie.
+    __device__ __forceinline__ bool mark()
+    {
+        const int tid = threadIdx.x;
         for (int i = tid; i < TT; i += kGateThreads)
-            s_first[i] = s_last[i] = -1;
+            s.first[i] = s.last[i] = -1;
         if (tid < 64) {
-            // Sequences that start at tok0 or later, and the one before them.
-            const uint32_t s = tok0 > 0 ? first_above(p.ends, p.seqs, (uint64_t)tok0 - 1) : 0;
+            // Sequences that start at `low` or later, and the one before them.
+            const uint32_t from = low > 0 ? first_above(p->ends, p->seqs, (uint64_t)low - 1) : 0;
             if (tid == 0)
-                s_seq = s;
+                s.seq = from;
         }
         __syncthreads();
-        const bool top = GRAD ? k == 0 : k == p.tiles - 1;      // what lies past the rows is the last tile's
-        for (uint32_t s = s_seq + tid;; s += kGateThreads) {
-            bool more = s < p.seqs;
+        const bool top = GRAD ? k == 0 : k == p->tiles - 1;      // what lies past the rows is the last tile's
+        for (uint32_t q = s.seq + tid;; q += kGateThreads) {
+            bool more = q < p->seqs;
             uint64_t first = 0, len = 0;
             if (more) {
-                run_of(p.ends, p.tokens, s, &first, &len);
-                more = top || (int64_t)first < tok0 + TT;
+                run_of(p->ends, p->tokens, q, &first, &len);
+                more = top || (int64_t)first < low + TT;
             }
             if (more && len) {
-                if ((int64_t)first >= tok0 && (int64_t)first < tok0 + TT)
-                    s_first[first - tok0] = (int32_t)s;
+                if ((int64_t)first >= low && (int64_t)first < low + TT)
+                    s.first[first - low] = (int32_t)q;
                 const int64_t l = (int64_t)(first + len) - 1;
-                if (l >= tok0 && l < tok0 + TT)
-                    s_last[l - tok0] = (int32_t)s;
-            } else if (more && p.state_out && (int64_t)first >= tok0) {
-                // An empty sequence passes its state (or its gradient) through.
-                const float *from = GRAD ? p.last : p.first;
-                const uint64_t b0 = (uint64_t)(chain % p.blocks) * C;
-                for (uint64_t c = b0; c < b0 + C && c < p.width; ++c)
-                    p.state_out[s * p.width + c] = from ? from[s * p.width + c] : 0.f;
+                if (l >= low && l < low + TT)
+                    s.last[l - low] = (int32_t)q;
+            }
+            if (p->state_out) {
+                const int lane = tid % 64;
+                const float *const from = GRAD ? p->last : p->first;
+                uint64_t empty = __ballot(more && len == 0 && (int64_t)first >= low);
+                while (empty) {
+                    const uint32_t which = q - lane + (uint32_t)__builtin_ctzll(empty);
+                    empty &= empty - 1;
+                    // (A packed batch's lines are its blocks.)
+                    const uint64_t past = (uint64_t)(chain + count) * C < p->width ? (uint64_t)(chain + count) * C
+                                                                                   : p->width;
+                    for (uint64_t c = (uint64_t)chain * C + lane; c < past; c += 64)
+                        p->state_out[which * p->width + c] = from ? from[which * p->width + c] : 0.f;
+                }
             }
             if (__syncthreads_count(more) < kGateThreads)
                 break;
         }
+        bool any = false;
+        for (int i = tid; i < TT; i += kGateThreads)
+            any |= s.first[i] >= 0 || s.last[i] >= 0;
+        return __syncthreads_or(any) != 0;
+    }
+
+    // From dh of a token, h before it and its x: the gradients, and what goes on.
+    __device__ __forceinline__ static float grad_of(const Gate &w, float dh, float before, float x, float *dg, float *dx)
+    {
+        *dx = BLEND ? dh * w.rest : dh;
+        const float da = dh * (BLEND ? before - x : before);
+        *dg = FORM == GATESCAN_DECAY ? da : FORM == GATESCAN_LOG ? da * w.a : da * (w.a * w.rest);
+        return w.a * dh;
+    }
+
+    // ---- Whole tiles: no sequence starts or ends in them (but for equal    ----
+    // ---- sequences' own ends, whose states the carry takes in), and every ----
+    // ---- lane has all of its channels or none.                            ----
+
+    // The same for all threads.
+    __device__ __forceinline__ bool whole() const
+    {
+        return low >= (GRAD ? 1 : 0) && low + TT <= (int64_t)end && p->width % V == 0;
+    }
+
+    struct Pieces {
+        piece_t g[R], d[R];          // gate; x, or dout in the gradient
+    };
+    template <class Rows>
+    __device__ __forceinline__ void load_rows(const Rows &from, uint32_t line, int lane8, int64_t first,
+                                              piece_t (&to)[R]) const
+    {
+        const int64_t step = GRAD ? -from.tok : from.tok;
+        const T *at = row(from, line, first) + lane8 * V;
+#pragma unroll
+        for (int r = 0; r < R; ++r, at += step)
+            to[r] = load_piece_past(at);
+    }
+
+    // 1. of a tile, from its rows; the forward pass keeps a and b for 3.
+    struct Kept {
+        float a[GRAD ? 1 : R][V], b[GRAD ? 1 : R][V];
+    };
+    __device__ __forceinline__ void scan(const Pieces &x, Kept &keep, int lane8, int group) const
+    {
+        float A[V], H[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            A[e] = 1.f;
+            H[e] = 0.f;
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (inside(r)) {
-                firsts |= (s_first[token(r) - tok0] >= 0 ? 1u : 0u) << r;
-                lasts |= (s_last[token(r) - tok0] >= 0 ? 1u : 0u) << r;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const Gate w = gate_of<FORM, FINE>(U::get(x.g[r], e));
+                if (GRAD) {
+                    H[e] = w.a * (H[e] + U::get(x.d[r], e));
+                } else {
+                    const float v = U::get(x.d[r], e);
+                    keep.a[r][e] = w.a;
+                    keep.b[r][e] = BLEND ? w.rest * v : v;
+                    H[e] = __builtin_fmaf(w.a, H[e], keep.b[r][e]);
+                }
+                A[e] *= w.a;
+            }
+            // Row by row: moved behind all rows' gates, the sums would need more
+            // registers than there are.
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                asm volatile("" : "+v"(A[e]), "+v"(H[e]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        bool gone = false;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            gone |= A[e] == 0.f;
+        if (__any(gone)) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                A[e] = 1.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    A[e] = kept_product<FORM == GATESCAN_DECAY>(
+                        A[e], GRAD ? gate_of<FORM, FINE>(U::get(x.g[r], e)).a : keep.a[GRAD ? 0 : r][e]);
             }
         }
-    } else {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            firsts |= (token(r) == 0 ? 1u : 0u) << r;
-            lasts |= (token(r) == (int64_t)end - 1 ? 1u : 0u) << r;
+        for (int e = 0; e < V; ++e)
+            s.a[group][lane8 * V + e] = A[e];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            s.h[group][lane8 * V + e] = H[e];
+    }
+
+    // 3. of a forward tile.
+    __device__ __forceinline__ void finish(const Kept &keep, uint32_t line, int lane8, int group, bool any) const
+    {
+        float H[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            H[e] = __builtin_fmaf(s.a[group][lane8 * V + e], s.carry[lane8 * V + e], s.h[group][lane8 * V + e]);
+        T *to = out_row(0, line, low + group * R) + lane8 * V;
+        if (any) {
+            const int64_t step = p->out_tok[0];
+#pragma unroll
+            for (int r = 0; r < R; ++r, to += step) {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    H[e] = __builtin_fmaf(keep.a[GRAD ? 0 : r][e], H[e], keep.b[GRAD ? 0 : r][e]);
+                store_piece_past(to, U::pack(H));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (p->state_out && !p->ends && group == G - 1 && low + TT == (int64_t)end)
+                store_floats<V>(p->state_out + (line / p->blocks) * p->width + column(line) + lane8 * V, V, H);
         }
     }
-    const auto out_at = [&](int i, int64_t t) {
-        return static_cast<T *>(p.out[i]) + (int64_t)seq * p.out_seq[i] + t * p.out_tok[i] + c0;
-    };
-    // Rows that are in no sequence.  A tile of nothing else is done: no tile
-    // with tokens looks back to it.
-    const auto clear = [&](int r) {
-        const int64_t t = token(r);
-        if (p.clear && n > 0 && t >= 0 && t < (int64_t)p.tokens) {
-            store_piece<T>(out_at(0, t), none, n);
+
+    __device__ __forceinline__ void stream_whole()
+    {
+        const int lane8 = threadIdx.x % kGateLanes, group = threadIdx.x / kGateLanes;
+        const int64_t first = token(group * R);
+        const auto any = [&](uint32_t line) { return column(line) + lane8 * V < p->width; };
+        for (uint32_t line = chain; line < chain + count; ++line) {
+            const bool mine = any(line);
+            Pieces x = {};
+            if (mine) {
+                load_rows(p->gate, line, lane8, first, x.g);
+                load_rows(GRAD ? p->dout : p->x, line, lane8, first, x.d);
+            }
+            if constexpr (!GRAD) {
+                Kept keep;
+                scan(x, keep, lane8, group);
+                __syncthreads();
+                if (threadIdx.x < 64) {
+                    stash(keep);
+                    carry(line, G, 0);
+                    unstash(keep);
+                }
+                __syncthreads();
+                finish(keep, line, lane8, group, mine);
+            } else {
+                Kept none;
+                scan(x, none, lane8, group);
+                piece_t rx[R] = {}, rh[R] = {};
+                const auto late = [&]() {
+                    if (BLEND)
+                        load_rows(p->x, line, lane8, first, rx);
+                    load_rows(p->h, line, lane8, first - 1, rh);
+                };
+                // The carrying wave's own come after its looks back: loads land
+                // in their order.
+                if (mine && threadIdx.x >= 64)
+                    late();
+                __syncthreads();
+                if (threadIdx.x < 64) {
+                    stash(x);
+                    carry(line, G, 0);
+                    unstash(x);
+                    if (mine)
+                        late();
+                }
+                __syncthreads();
+                float H[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    H[e] = __builtin_fmaf(s.a[group][lane8 * V + e], s.carry[lane8 * V + e],
+                                          s.h[group][lane8 * V + e]);
+                if (!mine)
+                    continue;
+                T *to = out_row(0, line, first) + lane8 * V, *to1 = out_row(1, line, first) + lane8 * V;
+                const int64_t step = -p->out_tok[0], step1 = -p->out_tok[1];
+#pragma unroll
+                for (int r = 0; r < R; ++r, to += step, to1 += step1) {
+                    float dg[V], dx[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const Gate w = gate_of<FORM, FINE>(U::get(x.g[r], e));
+                        H[e] = grad_of(w, U::get(x.d[r], e) + H[e], U::get(rh[r], e), BLEND ? U::get(rx[r], e) : 0.f,
+                                       &dg[e], &dx[e]);
+                    }
+                    store_piece_past(to, U::pack(dg));
+                    store_piece_past(to1, U::pack(dx));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
+
+    // What the carrying wave's threads keep of their tile, in LDS while they
+    // carry: their registers are full of it.
+    template <class X>
+    __device__ __forceinline__ void stash(const X &x) const
+    {
+        static_assert(sizeof(X) <= sizeof(s.kept[0]) * kStash, "room for it");
+        const piece_t *const from = reinterpret_cast<const piece_t *>(&x);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(X) / 16); ++i)
+            s.kept[i][threadIdx.x % 64] = from[i];
+    }
+    template <class X>
+    __device__ __forceinline__ void unstash(X &x) const
+    {
+        // By an address that says nothing of what was stored there.
+        uint32_t lane = threadIdx.x % 64;
+        asm volatile("" : "+v"(lane)::"memory");
+        piece_t *const to = reinterpret_cast<piece_t *>(&x);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(X) / 16); ++i)
+            to[i] = s.kept[i][lane];
+    }
+
+    // ---- Any tile ----
+
+    // The sequence that starts (ends) at a token, or -1.
+    __device__ __forceinline__ int64_t first_at(uint32_t line, int64_t t) const
+    {
+        return p->ends ? s.first[t - low] : t == 0 ? (int64_t)(line / p->blocks) : -1;
+    }
+    __device__ __forceinline__ int64_t last_at(uint32_t line, int64_t t) const
+    {
+        return p->ends ? s.last[t - low] : t == (int64_t)end - 1 ? (int64_t)(line / p->blocks) : -1;
+    }
+
+    // A thread's four channels of a line, from `c` on: at the width's end they
+    // overlap the four before, whose values they have as well.  n: how many
+    // there are, 4 unless the line has fewer, or 0.
+    __device__ __forceinline__ void four_of(uint32_t line, int *c, int *n) const
+    {
+        const uint64_t rest = p->width - column(line);
+        const int left = rest < (uint64_t)C ? (int)rest : C;
+        *c = threadIdx.x % (C / 4) * 4;
+        *n = *c >= left ? 0 : left < 4 ? left : 4;
+        if (*n == 4 && *c > left - 4)
+            *c = left - 4;
+    }
+
+    __device__ __forceinline__ void stream_any(uint32_t line)
+    {
+        const int part = threadIdx.x / (C / 4);
+        int c, n;
+        four_of(line, &c, &n);
+        const uint64_t at = column(line) + c;
+        const auto state_of = [&](const float *of, int64_t q, float (&to)[4]) {
+            const piece_t v = of ? load_piece<float>(of + q * (int64_t)p->width + (int64_t)at, n) : piece_t{0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                to[e] = Unpack<float>::get(v, e);
+        };
+        Four<T> g[kTokens], d[kTokens], x[GRAD ? kTokens : 1], h[GRAD ? kTokens : 1];
+        (void)x;
+        (void)h;
+        uint32_t in = 0, firsts = 0, lasts = 0;      // a bit a token
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u) {
+            const int64_t t = token(part * kTokens + u);
+            const bool inside = n > 0 && t >= 0 && t < (int64_t)end;
+            g[u] = d[u] = Four<T>{};
+            if (inside) {
+                g[u] = load_four(row(p->gate, line, t) + c, n);
+                d[u] = load_four(row(GRAD ? p->dout : p->x, line, t) + c, n);
+                in |= 1u << u;
+                firsts |= (first_at(line, t) >= 0 ? 1u : 0u) << u;
+                lasts |= (last_at(line, t) >= 0 ? 1u : 0u) << u;
+            }
+            if constexpr (GRAD) {
+                x[u] = h[u] = Four<T>{};
+                if (inside) {
+                    if (BLEND)
+                        x[u] = load_four(row(p->x, line, t) + c, n);
+                    if (t > 0)
+                        h[u] = load_four(row(p->h, line, t - 1) + c, n);
+                }
+            }
+        }
+        const uint32_t resets = GRAD ? lasts : firsts;       // where the sweep starts anew
+        float A[4], H[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            A[e] = 1.f;
+            H[e] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u) {
+            const int64_t t = token(part * kTokens + u);
+            if (!(in >> u & 1))
+                continue;
+            if (resets >> u & 1)
+                state_of(GRAD ? p->last : p->first, GRAD ? last_at(line, t) : first_at(line, t), H);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Gate w = gate_of<FORM, FINE>(g[u].get(e));
+                const float v = d[u].get(e);
+                H[e] = GRAD ? w.a * (H[e] + v) : __builtin_fmaf(w.a, H[e], BLEND ? w.rest * v : v);
+                A[e] = kept_product<FORM == GATESCAN_DECAY>(A[e], w.a);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                asm volatile("" : "+v"(A[e]), "+v"(H[e]));
+        }
+        if (n > 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s.a[part][c + e] = A[e];
+                s.h[part][c + e] = H[e];
+            }
+        }
+        if (threadIdx.x % (C / 4) == 0)          // a line's first channel is one of the width's
+            s.reset[part] = resets != 0;
+        __syncthreads();
+        const uint32_t anew = parts_anew();
+        if (threadIdx.x < 64)
+            carry(line, kParts, anew);
+        __syncthreads();
+        const bool started = (anew & ((1u << part) - 1)) != 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            H[e] = started ? s.h[part][c + e] : __builtin_fmaf(s.a[part][c + e], s.carry[c + e], s.h[part][c + e]);
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u) {
+            const int64_t t = token(part * kTokens + u);
+            if (!(in >> u & 1)) {
+                clear(line, t, c, n);
+                continue;
+            }
+            if (resets >> u & 1)
+                state_of(GRAD ? p->last : p->first, GRAD ? last_at(line, t) : first_at(line, t), H);
+            float out[2][4], before[4];
+            if constexpr (GRAD) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    before[e] = h[u].get(e);
+                if (firsts >> u & 1)
+                    state_of(p->first, first_at(line, t), before);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Gate w = gate_of<FORM, FINE>(g[u].get(e));
+                const float v = d[u].get(e);
+                if constexpr (GRAD)
+                    H[e] = grad_of(w, v + H[e], before[e], BLEND ? x[u].get(e) : 0.f, &out[0][e], &out[1][e]);
+                else
+                    out[0][e] = H[e] = __builtin_fmaf(w.a, H[e], BLEND ? w.rest * v : v);
+            }
+            store_four(out_row(0, line, t) + c, Four<T>::of(out[0]), n);
+            if constexpr (GRAD)
+                store_four(out_row(1, line, t) + c, Four<T>::of(out[1]), n);
+            if (p->state_out && ((GRAD ? firsts : lasts) >> u & 1))
+                store_piece<float>(p->state_out + (GRAD ? first_at(line, t) : last_at(line, t)) * (int64_t)p->width +
+                                       (int64_t)at, Unpack<float>::pack(H), n);
+        }
+    }
+    // Rows that are in no sequence.
+    __device__ __forceinline__ void clear(uint32_t line, int64_t t, int c, int n) const
+    {
+        if (p->clear && n > 0 && t >= (int64_t)end && t < (int64_t)p->tokens) {
+            store_four(out_row(0, line, t) + c, Four<T>{}, n);
             if (GRAD)
-                store_piece<T>(out_at(1, t), none, n);
+                store_four(out_row(1, line, t) + c, Four<T>{}, n);
         }
-    };
-    if ((tok0 > 0 ? tok0 : 0) >= (int64_t)end) {
-        for (int r = 0; r < R; ++r)
-            clear(r);
-        // Equal sequences of no tokens pass their states through.
-        if (!p.ends && p.state_out && group == 0 && n > 0) {
-            float v[V] = {};
-            const float *from = GRAD ? p.last : p.first;
-            if (from)
-                load_floats<V>(from + seq * p.width + c0, n, v);
-            store_floats<V>(p.state_out + seq * p.width + c0, n, v);
-        }
-        return;
     }
-    const auto seq_of = [&](const int32_t *marks, int r) -> uint64_t {
-        return p.ends ? (uint64_t)(uint32_t)marks[token(r) - tok0] : seq;
-    };
-    const uint32_t resets = GRAD ? lasts : firsts;       // where the sweep starts anew
-    // A wave without starts, ends and rows outside takes the short way.
-    const bool plain = !__any(!whole || (firsts | lasts) != 0);
+    __device__ __forceinline__ uint32_t parts_anew() const
+    {
+        const uint32_t lane = threadIdx.x % 64;
+        return (uint32_t)__ballot(lane < (uint32_t)kParts && s.reset[lane % kParts] != 0);
+    }
 
-    // The thread's own tokens: (A, H) of each channel.
-    float A[V], H[V];
-    bool zero[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        A[e] = 1.f;
-        H[e] = 0.f;
-        zero[e] = false;
+    // A tile without tokens: none with any looks back to it.  Equal sequences of
+    // no tokens pass their states through.
+    __device__ __forceinline__ bool idle() const { return (low > 0 ? low : 0) >= (int64_t)end; }
+    __device__ __forceinline__ void stream_idle(uint32_t line) const
+    {
+        const int part = threadIdx.x / (C / 4);
+        int c, n;
+        four_of(line, &c, &n);
+        const uint64_t at = column(line) + c;
+        for (int u = 0; u < kTokens; ++u)
+            clear(line, token(part * kTokens + u), c, n);
+        if (!p->ends && p->state_out && part == 0) {
+            const float *const from = GRAD ? p->last : p->first;
+            const uint64_t of = (line / p->blocks) * p->width + at;
+            store_piece<float>(p->state_out + of, from ? load_piece<float>(from + of, n) : piece_t{0, 0, 0, 0}, n);
+        }
     }
-    float fa[GRAD ? 1 : R][V], fb[GRAD ? 1 : R][V];      // forward: a and b, kept for the second pass
-    (void)fa;
-    (void)fb;
+
+    // 2., by one wave: the groups' pairs, the tile's carry.  anew: the groups in
+    // which the sweep starts anew, a bit each.
+    __device__ __forceinline__ void carry(uint32_t line, int groups, uint32_t anew)
+    {
+        const uint32_t tag = __builtin_amdgcn_readfirstlane(s.tag);
+        const int lane = threadIdx.x % 64;
+        if (lane >= C)
+            return;
+        // The first tile of the line that has tokens starts a sequence, and
+        // equal sequences' states enter there.
+        const uint32_t k0 = GRAD && p->ends ? (uint32_t)((p->tokens - end) / TT) : 0;
+        // The nearest tiles' words: asked for before the groups are chained, as
+        // mostly a tile shortly before is through by then.
+        const Window<4> w = window<4>(line, k0, lane);
+        float in = 0.f, a = 1.f, h = 0.f;
+        // (Eight at a time: one by one each read of LDS waits for the write before it.)
+        for (int g0 = 0; g0 < groups; g0 += 8) {
+            float ga[8], gh[8], ea[8], eh[8];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (!plain && !inside(r)) {
-            if (!GRAD) {
+            for (int u = 0; u < 8; ++u) {
+                ga[u] = s.a[g0 + u][lane];
+                gh[u] = s.h[g0 + u][lane];
+            }
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    fa[r][e] = 1.f;
-                    fb[r][e] = 0.f;
+            for (int u = 0; u < 8; ++u) {
+                ea[u] = a;
+                eh[u] = h;
+                h = __builtin_fmaf(ga[u], h, gh[u]);
+                a = kept_product<FORM == GATESCAN_DECAY>(a, ga[u]);
+            }
+            if (anew >> g0 & 0xFF) {
+                h = eh[0];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    eh[u] = h;
+                    h = anew >> (g0 + u) & 1 ? gh[u] : __builtin_fmaf(ga[u], h, gh[u]);
                 }
             }
-            continue;
-        }
-        const bool reset = !plain && (resets >> r & 1) != 0;
-        float from[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            from[e] = 0.f;
-        if (reset) {
-            const float *s = GRAD ? p.last : p.first;
-            if (s)
-                load_floats<V>(s + seq_of(GRAD ? s_last : s_first, r) * p.width + c0, n, from);
+            for (int u = 0; u < 8; ++u) {
+                s.a[g0 + u][lane] = ea[u];
+                s.h[g0 + u][lane] = eh[u];
+            }
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const Gate w = gate_of<FORM>(U::get(rg[r], e));
-            if (GRAD) {
-                const float d = U::get(rd[r], e);
-                H[e] = w.a * ((reset ? from[e] : H[e]) + d);
+        uint64_t *const mine = p->desc + ((uint64_t)(k * p->chains + line) * 2) * C + lane;      // A; H is C on
+        if (k > k0 && !nearest(w, tag, &in)) {
+            if (anew != 0) {
+                send(mine + C, tag | kStatusPrefix, h);
             } else {
-                const float x = U::get(rx[r], e), b = BLEND ? w.rest * x : x;
-                // A sequence's first token takes in the state before it.
-                fa[r][e] = w.a;
-                H[e] = __builtin_fmaf(w.a, reset ? from[e] : H[e], b);
-                fb[r][e] = reset ? H[e] : b;
+                send(mine, tag | kStatusAgg, a);
+                send(mine + C, tag | kStatusAgg, h);
             }
-            A[e] = reset ? 0.f : A[e] * w.a;
-            zero[e] |= w.a == 0.f;
+            for (;;) {
+                if (p->far ? nearest(window<kGateWindow>(line, k0, lane), tag, &in)
+                           : nearest(window<4>(line, k0, lane), tag, &in))
+                    break;
+            }
+            if (anew == 0)
+                send(mine + C, tag | kStatusPrefix, __builtin_fmaf(a, in, h));
+        } else if (p->tiles > 1) {
+            if (k <= k0)
+                in = entering(line, lane);
+            send(mine + C, tag | kStatusPrefix, anew != 0 ? h : __builtin_fmaf(a, in, h));
+        } else {
+            in = entering(line, lane);
         }
+        s.carry[lane] = in;
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        s_a[group][lane8 * V + e] = kept_product(A[e], zero[e]);
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        s_h[group][lane8 * V + e] = H[e];
-    if (lane8 == 0)
-        s_reset[group] = resets;
-    __syncthreads();
 
-    // One lane a channel: the tile's pair, the carry, and each group's.
-    if (tid < C) {
-        const uint64_t anew = __ballot(tid < G && s_reset[tid % G] != 0);
-        // The first tile of the line that has tokens starts a sequence.
-        const uint32_t k0 = GRAD && p.ends ? (uint32_t)((p.tokens - end) / TT) : 0;
-        uint64_t *const mine = p.desc + ((uint64_t)at * 2) * C + tid;      // A; H is C further on
-        float carry = 0.f;
-        if (chained) {
-            float a = 1.f, h = 0.f;
-            bool none_zero = true;
-#pragma unroll 8
-            for (int g = 0; g < G; ++g) {
-                const float ga = s_a[g][tid], gh = s_h[g][tid];
-                if (anew >> g & 1) {
-                    a = 0.f;
-                    h = gh;
-                } else {
-                    a *= ga;
-                    h = __builtin_fmaf(ga, h, gh);
-                }
-                none_zero = none_zero && ga != 0.f;
-            }
-            const bool known = anew != 0 || k <= k0;
-            const auto word = [&](uint32_t status, float v) {
-                return (uint64_t)(tag | status) << 32 | __builtin_bit_cast(uint32_t, v);
-            };
-            const auto put = [&](uint64_t *to, uint64_t w) {
-                __hip_atomic_store(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            };
-            const auto get = [&](uint32_t tile, int half) {
-                return __hip_atomic_load(p.desc + ((uint64_t)(tile * p.chains + chain) * 2 + half) * C + tid,
-                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            };
-            const auto status = [&](uint64_t w) {
-                const uint32_t hi = (uint32_t)(w >> 32);
-                return (hi & ~3u) == tag ? hi & 3u : 0u;
-            };
-            const auto value = [&](uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); };
-            if (known) {
-                put(mine + C, word(kStatusPrefix, h));
-            } else {
-                put(mine, word(kStatusAgg, kept_product(a, !none_zero)));
-                put(mine + C, word(kStatusAgg, h));
-            }
-            if (k > k0) {
-                // The nearest tile whose chained value is there, among the
-                // last kWindow, with the pairs of all between.
-                constexpr int kStep = 4, kWindow = 32;
-                uint64_t wa[kStep], wh[kStep];
-                int found = -1;
-                while (found < 0) {
-                    for (int b = 0; b < kWindow && found < 0; b += kStep) {
-                        bool ready = true;
-#pragma unroll
-                        for (int i = 0; i < kStep; ++i) {
-                            const uint32_t back = (uint32_t)(b + i) < k - k0 ? b + i : k - k0 - 1;
-                            wh[i] = get(k - 1 - back, 1);
-                            wa[i] = b == 0 ? get(k - 1 - back, 0) : 0;
-                        }
-#pragma unroll
-                        for (int i = 0; i < kStep; ++i) {
-                            if (found < 0 && ready) {
-                                if (__all(status(wh[i]) == kStatusPrefix))
-                                    found = b + i;
-                                else
-                                    ready = __all(status(wh[i]) != 0 && (b != 0 || status(wh[i]) == kStatusPrefix ||
-                                                                         status(wa[i]) != 0));
-                            }
-                        }
-                        if (!ready)
-                            break;
-                    }
-                    if (found < 0)
-                        __builtin_amdgcn_s_sleep(1);
-                }
-                if (found < kStep) {
-#pragma unroll
-                    for (int i = kStep - 1; i >= 0; --i) {
-                        if (i <= found)
-                            carry = status(wh[i]) == kStatusPrefix
-                                        ? value(wh[i])
-                                        : __builtin_fmaf(value(wa[i]), carry, value(wh[i]));
-                    }
-                } else {
-                    for (int b = found; b >= 0; b -= kStep) {
-                        bool ready = false;
-                        while (!ready) {
-                            ready = true;
-#pragma unroll
-                            for (int i = 0; i < kStep; ++i) {
-                                const uint32_t tile = k - 1 - (b - i > 0 ? b - i : 0);
-                                wh[i] = get(tile, 1);
-                                wa[i] = get(tile, 0);
-                            }
-#pragma unroll
-                            for (int i = 0; i < kStep; ++i)
-                                ready = ready && status(wh[i]) != 0 &&
-                                        (status(wh[i]) == kStatusPrefix || status(wa[i]) != 0);
-                            ready = __all(ready);
-                        }
-#pragma unroll
-                        for (int i = 0; i < kStep; ++i) {
-                            if (b - i >= 0)
-                                carry = status(wh[i]) == kStatusPrefix
-                                            ? value(wh[i])
-                                            : __builtin_fmaf(value(wa[i]), carry, value(wh[i]));
-                        }
-                    }
-                }
-                if (!known)
-                    put(mine + C, word(kStatusPrefix, __builtin_fmaf(kept_product(a, !none_zero), carry, h)));
-            }
-        }
-#pragma unroll 8
-        for (int g = 0; g < G; ++g) {
-            const float ga = s_a[g][tid], gh = s_h[g][tid];
-            s_h[g][tid] = carry;
-            carry = anew >> g & 1 ? gh : __builtin_fmaf(ga, carry, gh);
-        }
+    // What enters the first tile of equal sequences.
+    __device__ __forceinline__ float entering(uint32_t line, int lane) const
+    {
+        const float *const state = GRAD ? p->last : p->first;
+        const uint64_t c = column(line) + lane;
+        return !p->ends && state && c < p->width ? state[(line / p->blocks) * p->width + c] : 0.f;
     }
-    __syncthreads();
 
-    // Once more over the thread's tokens, from what enters them.
+    // The words of the N tiles before this one (of the line's first, where there are fewer).
+    template <int N>
+    struct Window {
+        uint64_t a[N], h[N];
+    };
+    template <int N>
+    __device__ __forceinline__ Window<N> window(uint32_t line, uint32_t k0, int lane) const
+    {
+        Window<N> w;
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-        H[e] = s_h[group][lane8 * V + e];
-    if (n == 0)
-        return;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t t = token(r);
-        if (!plain && !inside(r)) {
-            clear(r);
-            continue;
+        for (int u = 0; u < N; ++u) {
+            const uint32_t tile = k > k0 + u ? k - 1 - u : k0;
+            w.h[u] = fetch(line, tile, 1, lane);
+            w.a[u] = fetch(line, tile, 0, lane);
         }
-        const bool reset = !plain && (resets >> r & 1) != 0;
-        if (!GRAD) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                H[e] = reset ? fb[r][e] : __builtin_fmaf(fa[r][e], H[e], fb[r][e]);
-            store_piece<T>(out_at(0, t), U::pack(H), n);
-            if (!plain && (lasts >> r & 1) && p.state_out)
-                store_floats<V>(p.state_out + seq_of(s_last, r) * p.width + c0, n, H);
-            continue;
-        }
-        const bool starts = !plain && (firsts >> r & 1) != 0;
-        if (reset) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                H[e] = 0.f;
-            if (p.last)
-                load_floats<V>(p.last + seq_of(s_last, r) * p.width + c0, n, H);
-        }
-        float before[V], dg[V], dx[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            before[e] = U::get(rh[r], e);
-        if (starts) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                before[e] = 0.f;
-            if (p.first)
-                load_floats<V>(p.first + seq_of(s_first, r) * p.width + c0, n, before);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const Gate w = gate_of<FORM>(U::get(rg[r], e));
-            const float dh = U::get(rd[r], e) + H[e];
-            H[e] = w.a * dh;
-            dx[e] = BLEND ? dh * w.rest : dh;
-            const float da = dh * (BLEND ? before[e] - U::get(rx[r], e) : before[e]);
-            dg[e] = FORM == GATESCAN_DECAY ? da : FORM == GATESCAN_LOG ? da * w.a : da * (w.a * w.rest);
-        }
-        store_piece<T>(out_at(0, t), U::pack(dg), n);
-        store_piece<T>(out_at(1, t), U::pack(dx), n);
-        if (starts && p.state_out)
-            store_floats<V>(p.state_out + seq_of(s_first, r) * p.width + c0, n, H);
+        return w;
     }
+    // What enters this tile, if the window has a chained value and all pairs after it.
+    template <int N>
+    __device__ __forceinline__ static bool nearest(const Window<N> &w, uint32_t tag, float *in)
+    {
+        uint32_t chained = 0, ready = 0;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint32_t st = status(w.h[u], tag);
+            chained |= (uint32_t)__all(st == kStatusPrefix) << u;
+            ready |= (uint32_t)__all(st == kStatusPrefix || (st != 0 && status(w.a[u], tag) != 0)) << u;
+        }
+        const uint32_t first = chained & (0u - chained);
+        if (chained == 0 || (~ready & (first - 1)) != 0)
+            return false;
+        float x = 0.f;
+#pragma unroll
+        for (int u = N - 1; u >= 0; --u)
+            if (1u << u <= first)
+                x = advance(x, w.a[u], w.h[u], tag);
+        *in = x;
+        return true;
+    }
+
+    __device__ __forceinline__ static void send(uint64_t *to, uint32_t head, float v)
+    {
+        __hip_atomic_store(to, (uint64_t)head << 32 | __builtin_bit_cast(uint32_t, v), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ uint64_t fetch(uint32_t line, uint32_t tile, int half, int lane) const
+    {
+        return __hip_atomic_load(p->desc + ((uint64_t)(tile * p->chains + line) * 2 + half) * C + lane,
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ static uint32_t status(uint64_t w, uint32_t tag)
+    {
+        const uint32_t hi = (uint32_t)(w >> 32);
+        return (hi & ~3u) == tag ? hi & 3u : 0u;
+    }
+    __device__ __forceinline__ static float value(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); }
+    // One tile further: its chained value, or its pair on top of what enters it.
+    __device__ __forceinline__ static float advance(float in, uint64_t wa, uint64_t wh, uint32_t tag)
+    {
+        return status(wh, tag) == kStatusPrefix ? value(wh) : __builtin_fmaf(value(wa), in, value(wh));
+    }
+
+    __device__ __forceinline__ void run()
+    {
+        if (!(p->ends && mark()) && whole()) {
+            stream_whole();
+            return;
+        }
+        for (uint32_t line = chain; line < chain + count; ++line) {
+            if (idle())
+                stream_idle(line);
+            else
+                stream_any(line);
+        }
+    }
+};
+
+template <class T, int FORM, bool BLEND, bool GRAD>
+__global__ __launch_bounds__(kGateThreads, 4) void gatescan_kernel(GateArgs p)
+{
+    typedef GateTile<T, FORM, BLEND, GRAD> Tile;
+    __shared__ typename Tile::Shared s;
+    uint32_t number = blockIdx.x;                    // lines of one tile wait for nothing
+    if (p.tiles > 1) {
+        if (threadIdx.x == 0) {
+            const TileTicket t = draw_ticket(p.ticket, p.draws);
+            s.draw = t.tile;
+            s.tag = t.tag;
+        }
+        __syncthreads();
+        number = __builtin_amdgcn_readfirstlane(s.draw);
+    }
+    Tile(s, number).run();
 }
 
 template <class T, bool GRAD>
 hipError_t launch_gate_tiles(const GateArgs &a, hipStream_t stream)
 {
-    const unsigned grid = a.chains * a.tiles;
 #define LIBSCAN_GATE(FORM)                                                                        \
     if (a.form == FORM) {                                                                         \
         if (a.blend)                                                                              \
-            gatescan_kernel<T, FORM, true, GRAD><<<grid, kGateThreads, 0, stream>>>(a);           \
+            gatescan_kernel<T, FORM, true, GRAD><<<a.draws, kGateThreads, 0, stream>>>(a);        \
         else                                                                                      \
-            gatescan_kernel<T, FORM, false, GRAD><<<grid, kGateThreads, 0, stream>>>(a);          \
+            gatescan_kernel<T, FORM, false, GRAD><<<a.draws, kGateThreads, 0, stream>>>(a);       \
     }
     LIBSCAN_GATE(GATESCAN_DECAY)
     LIBSCAN_GATE(GATESCAN_LOG)
