@@ -103,7 +103,8 @@ struct GateTile {
     static constexpr int kParts = kGateThreads * 4 / C, kTokens = TT / kParts;
     static_assert(C <= 64 && kParts <= G && G <= 32 && G % 8 == 0 && kParts % 8 == 0, "one wave chains the groups");
 
-    static constexpr int kStash = GRAD ? 2 * R : R * V / 2;      // pieces that a thread keeps
+    // Pieces that a thread keeps of a tile.
+    static constexpr int kStash = GRAD ? 3 * R + (BLEND ? R : 1) : R * V / 2;
 
     struct Shared {
         // Each group's pair, then that of all groups before it in the tile.
@@ -122,7 +123,8 @@ struct GateTile {
     Args *p;
     Shared &s;
     uint64_t end;                // tokens [0, end) are in sequences
-    uint32_t k, chain, count;    // the workgroup's tiles: `count` lines from `chain` on
+    uint32_t k, chain, count;    // the workgroup's tiles: of `count` lines from `chain` on
+    uint32_t line, tid;          // the one under way; the thread
     int64_t low;                 // their lowest token (below 0 where a gradient's last tile reaches past them)
 
     __device__ __forceinline__ GateTile(Shared &shared, uint32_t number) : s(shared)
@@ -143,20 +145,19 @@ struct GateTile {
     // The token at one of the tile's places in the sweep's order.
     __device__ __forceinline__ int64_t token(int at) const { return GRAD ? low + (TT - 1 - at) : low + at; }
 
-    // Where a line's channels start, and how many of them a thread has that
-    // starts `at` into them.
-    __device__ __forceinline__ uint64_t column(uint32_t line) const { return (uint64_t)(line % p->blocks) * C; }
+    // Where the line's channels start.
+    __device__ __forceinline__ uint64_t column() const { return (uint64_t)(line % p->blocks) * C; }
 
     template <class Rows>
-    __device__ __forceinline__ const T *row(const Rows &from, uint32_t line, int64_t t) const
+    __device__ __forceinline__ const T *row(const Rows &from, int64_t t) const
     {
         return static_cast<const T *>(from.p) + (int64_t)(line / p->blocks) * from.seq + t * from.tok +
-               (int64_t)column(line);
+               (int64_t)column();
     }
-    __device__ __forceinline__ T *out_row(int which, uint32_t line, int64_t t) const
+    __device__ __forceinline__ T *out_row(int which, int64_t t) const
     {
         return static_cast<T *>(p->out[which]) + (int64_t)(line / p->blocks) * p->out_seq[which] +
-               t * p->out_tok[which] + (int64_t)column(line);
+               t * p->out_tok[which] + (int64_t)column();
     }
 
     // Where sequences start and end among the tile's tokens, and whether any
@@ -228,21 +229,35 @@ struct GateTile {
     // The same for all threads.
     __device__ __forceinline__ bool whole() const
     {
-        return low >= (GRAD ? 1 : 0) && low + TT <= (int64_t)end && p->width % V == 0;
+        // (A packed batch's first token starts a sequence, so that low > 0 there.)
+        return low >= 0 && low + TT <= (int64_t)end && p->width % V == 0;
     }
 
     struct Pieces {
-        piece_t g[R], d[R];          // gate; x, or dout in the gradient
+        piece_t g[R], d[R];                              // gate; x, or dout in the gradient
+        piece_t h[GRAD ? R : 1], x[GRAD && BLEND ? R : 1];
     };
     template <class Rows>
-    __device__ __forceinline__ void load_rows(const Rows &from, uint32_t line, int lane8, int64_t first,
+    __device__ __forceinline__ void load_rows(const Rows &from, int lane8, int64_t first,
                                               piece_t (&to)[R]) const
     {
         const int64_t step = GRAD ? -from.tok : from.tok;
-        const T *at = row(from, line, first) + lane8 * V;
+        const T *at = row(from, first) + lane8 * V;
 #pragma unroll
         for (int r = 0; r < R; ++r, at += step)
             to[r] = load_piece_past(at);
+    }
+
+    // The forward pass's outputs a token earlier; in place of those before the
+    // first token, which are its state, its own.
+    template <class To>
+    __device__ __forceinline__ void load_before(int lane8, int64_t first, To &to) const
+    {
+        const int64_t tok = p->h.tok;
+        const T *at = row(p->h, first - 1) + lane8 * V;
+#pragma unroll
+        for (int r = 0; r < R; ++r, at -= tok)
+            to[r] = load_piece_past(r == R - 1 && first == R - 1 ? at + tok : at);
     }
 
     // 1. of a tile, from its rows; the forward pass keeps a and b for 3.
@@ -302,13 +317,13 @@ struct GateTile {
     }
 
     // 3. of a forward tile.
-    __device__ __forceinline__ void finish(const Kept &keep, uint32_t line, int lane8, int group, bool any) const
+    __device__ __forceinline__ void finish(const Kept &keep, int lane8, int group, bool any) const
     {
         float H[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
             H[e] = __builtin_fmaf(s.a[group][lane8 * V + e], s.carry[lane8 * V + e], s.h[group][lane8 * V + e]);
-        T *to = out_row(0, line, low + group * R) + lane8 * V;
+        T *to = out_row(0, low + group * R) + lane8 * V;
         if (any) {
             const int64_t step = p->out_tok[0];
 #pragma unroll
@@ -320,78 +335,81 @@ struct GateTile {
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (p->state_out && !p->ends && group == G - 1 && low + TT == (int64_t)end)
-                store_floats<V>(p->state_out + (line / p->blocks) * p->width + column(line) + lane8 * V, V, H);
+                store_floats<V>(p->state_out + (line / p->blocks) * p->width + column() + lane8 * V, V, H);
         }
     }
 
     __device__ __forceinline__ void stream_whole()
     {
-        const int lane8 = threadIdx.x % kGateLanes, group = threadIdx.x / kGateLanes;
+        const int lane8 = tid % kGateLanes, group = tid / kGateLanes;
         const int64_t first = token(group * R);
-        const auto any = [&](uint32_t line) { return column(line) + lane8 * V < p->width; };
-        for (uint32_t line = chain; line < chain + count; ++line) {
-            const bool mine = any(line);
-            Pieces x = {};
-            if (mine) {
-                load_rows(p->gate, line, lane8, first, x.g);
-                load_rows(GRAD ? p->dout : p->x, line, lane8, first, x.d);
+        const bool mine = column() + lane8 * V < p->width;
+        Pieces x = {};
+        if (mine) {
+            load_rows(p->gate, lane8, first, x.g);
+            load_rows(GRAD ? p->dout : p->x, lane8, first, x.d);
+        }
+        if constexpr (!GRAD) {
+            Kept keep;
+            scan(x, keep, lane8, group);
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                stash(keep);
+                carry(G, 0);
+                unstash(keep);
             }
-            if constexpr (!GRAD) {
-                Kept keep;
-                scan(x, keep, lane8, group);
-                __syncthreads();
-                if (threadIdx.x < 64) {
-                    stash(keep);
-                    carry(line, G, 0);
-                    unstash(keep);
-                }
-                __syncthreads();
-                finish(keep, line, lane8, group, mine);
-            } else {
-                Kept none;
-                scan(x, none, lane8, group);
-                piece_t rx[R] = {}, rh[R] = {};
-                const auto late = [&]() {
-                    if (BLEND)
-                        load_rows(p->x, line, lane8, first, rx);
-                    load_rows(p->h, line, lane8, first - 1, rh);
-                };
-                // The carrying wave's own come after its looks back: loads land
-                // in their order.
-                if (mine && threadIdx.x >= 64)
-                    late();
-                __syncthreads();
-                if (threadIdx.x < 64) {
-                    stash(x);
-                    carry(line, G, 0);
-                    unstash(x);
-                    if (mine)
-                        late();
-                }
-                __syncthreads();
-                float H[V];
+            __syncthreads();
+            finish(keep, lane8, group, mine);
+        } else {
+            if (mine) {
+                if constexpr (BLEND)
+                    load_rows(p->x, lane8, first, x.x);
+                load_before(lane8, first, x.h);
+            }
+            Kept none;
+            scan(x, none, lane8, group);
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                stash(x);
+                carry(G, 0);
+                unstash(x);
+            }
+            __syncthreads();
+            float H[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                H[e] = __builtin_fmaf(s.a[group][lane8 * V + e], s.carry[lane8 * V + e],
+                                      s.h[group][lane8 * V + e]);
+            if (!mine)
+                return;
+            T *to = out_row(0, first) + lane8 * V, *to1 = out_row(1, first) + lane8 * V;
+            const int64_t step = -p->out_tok[0], step1 = -p->out_tok[1];
+            const uint64_t of = (line / p->blocks) * p->width + column() + lane8 * V;      // in states
+#pragma unroll
+            for (int r = 0; r < R; ++r, to += step, to1 += step1) {
+                float dg[V], dx[V], before[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    H[e] = __builtin_fmaf(s.a[group][lane8 * V + e], s.carry[lane8 * V + e],
-                                          s.h[group][lane8 * V + e]);
-                if (!mine)
-                    continue;
-                T *to = out_row(0, line, first) + lane8 * V, *to1 = out_row(1, line, first) + lane8 * V;
-                const int64_t step = -p->out_tok[0], step1 = -p->out_tok[1];
+                    before[e] = U::get(x.h[r], e);
+                if (r == R - 1 && first == R - 1) {          // the first token of all
 #pragma unroll
-                for (int r = 0; r < R; ++r, to += step, to1 += step1) {
-                    float dg[V], dx[V];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const Gate w = gate_of<FORM, FINE>(U::get(x.g[r], e));
-                        H[e] = grad_of(w, U::get(x.d[r], e) + H[e], U::get(rh[r], e), BLEND ? U::get(rx[r], e) : 0.f,
-                                       &dg[e], &dx[e]);
-                    }
-                    store_piece_past(to, U::pack(dg));
-                    store_piece_past(to1, U::pack(dx));
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int e = 0; e < V; ++e)
+                        before[e] = 0.f;
+                    if (p->first)
+                        load_floats<V>(p->first + of, V, before);
                 }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const Gate w = gate_of<FORM, FINE>(U::get(x.g[r], e));
+                    H[e] = grad_of(w, U::get(x.d[r], e) + H[e], before[e], BLEND ? U::get(x.x[BLEND ? r : 0], e) : 0.f,
+                                   &dg[e], &dx[e]);
+                }
+                store_piece_past(to, U::pack(dg));
+                store_piece_past(to1, U::pack(dx));
+                __builtin_amdgcn_sched_barrier(0);
             }
+            if (p->state_out && first == R - 1)
+                store_floats<V>(p->state_out + of, V, H);
         }
     }
 
@@ -420,68 +438,94 @@ struct GateTile {
 
     // ---- Any tile ----
 
-    // The sequence that starts (ends) at a token, or -1.
-    __device__ __forceinline__ int64_t first_at(uint32_t line, int64_t t) const
-    {
-        return p->ends ? s.first[t - low] : t == 0 ? (int64_t)(line / p->blocks) : -1;
-    }
-    __device__ __forceinline__ int64_t last_at(uint32_t line, int64_t t) const
-    {
-        return p->ends ? s.last[t - low] : t == (int64_t)end - 1 ? (int64_t)(line / p->blocks) : -1;
-    }
-
     // A thread's four channels of a line, from `c` on: at the width's end they
     // overlap the four before, whose values they have as well.  n: how many
     // there are, 4 unless the line has fewer, or 0.
-    __device__ __forceinline__ void four_of(uint32_t line, int *c, int *n) const
+    __device__ __forceinline__ void four_of(int *c, int *n) const
     {
-        const uint64_t rest = p->width - column(line);
+        const uint64_t rest = p->width - column();
         const int left = rest < (uint64_t)C ? (int)rest : C;
-        *c = threadIdx.x % (C / 4) * 4;
+        *c = tid % (C / 4) * 4;
         *n = *c >= left ? 0 : left < 4 ? left : 4;
         if (*n == 4 && *c > left - 4)
             *c = left - 4;
     }
 
-    __device__ __forceinline__ void stream_any(uint32_t line)
+    // Rows of one tensor: the thread's first token's, and the way to its next.
+    struct Walk {
+        const T *at;
+        int64_t step;
+    };
+    template <class Rows>
+    __device__ __forceinline__ Walk walk(const Rows &from, int c, int64_t t) const
     {
-        const int part = threadIdx.x / (C / 4);
+        return Walk{row(from, t) + c, GRAD ? -from.tok : from.tok};
+    }
+
+    __device__ __forceinline__ void stream_any()
+    {
+        const int part = tid / (C / 4);
         int c, n;
-        four_of(line, &c, &n);
-        const uint64_t at = column(line) + c;
-        const auto state_of = [&](const float *of, int64_t q, float (&to)[4]) {
-            const piece_t v = of ? load_piece<float>(of + q * (int64_t)p->width + (int64_t)at, n) : piece_t{0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                to[e] = Unpack<float>::get(v, e);
-        };
-        Four<T> g[kTokens], d[kTokens], x[GRAD ? kTokens : 1], h[GRAD ? kTokens : 1];
-        (void)x;
-        (void)h;
+        four_of(&c, &n);
+        const int64_t at = (int64_t)column() + c, width = (int64_t)p->width;
+        // The thread's places and, by their distance from `low`, its tokens; of
+        // the tile's, those in [lo, hi) are in sequences.
+        const int lo = low < 0 ? (int)-low : 0, hi = (int64_t)end - low < TT ? (int)((int64_t)end - low) : TT;
+        const auto index = [&](int u) { return GRAD ? TT - 1 - (part * kTokens + u) : part * kTokens + u; };
+        const int64_t t0 = low + index(0);
         uint32_t in = 0, firsts = 0, lasts = 0;      // a bit a token
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
-            const int64_t t = token(part * kTokens + u);
-            const bool inside = n > 0 && t >= 0 && t < (int64_t)end;
-            g[u] = d[u] = Four<T>{};
-            if (inside) {
-                g[u] = load_four(row(p->gate, line, t) + c, n);
-                d[u] = load_four(row(GRAD ? p->dout : p->x, line, t) + c, n);
-                in |= 1u << u;
-                firsts |= (first_at(line, t) >= 0 ? 1u : 0u) << u;
-                lasts |= (last_at(line, t) >= 0 ? 1u : 0u) << u;
-            }
-            if constexpr (GRAD) {
-                x[u] = h[u] = Four<T>{};
-                if (inside) {
-                    if (BLEND)
-                        x[u] = load_four(row(p->x, line, t) + c, n);
-                    if (t > 0)
-                        h[u] = load_four(row(p->h, line, t - 1) + c, n);
-                }
+            const int i = index(u);
+            const bool inside = n > 0 && i >= lo && i < hi;
+            in |= (inside ? 1u : 0u) << u;
+            if (p->ends) {
+                firsts |= (inside && s.first[i] >= 0 ? 1u : 0u) << u;
+                lasts |= (inside && s.last[i] >= 0 ? 1u : 0u) << u;
             }
         }
+        if (!p->ends) {
+            // Equal sequences: at their ends' distances alone.
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u) {
+                firsts |= ((int64_t)index(u) == -low ? 1u : 0u) << u;
+                lasts |= ((int64_t)index(u) == (int64_t)end - 1 - low ? 1u : 0u) << u;
+            }
+            firsts &= in;
+            lasts &= in;
+        }
         const uint32_t resets = GRAD ? lasts : firsts;       // where the sweep starts anew
+        // The states of the sequence that starts (ends) at a place.
+        const auto place_of = [&](const int32_t *marks, int u) {
+            return (p->ends ? (int64_t)marks[index(u)] : (int64_t)(line / p->blocks)) * width + at;
+        };
+        const auto state_at = [&](const float *of, const int32_t *marks, int u, float (&to)[4]) {
+            const Four<float> v = of ? load_four(of + place_of(marks, u), n) : Four<float>{};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                to[e] = v.get(e);
+        };
+        const int32_t *const marks = GRAD ? s.last : s.first;
+        const float *const entering = GRAD ? p->last : p->first;
+
+        Four<T> g[kTokens], d[kTokens], x[GRAD && BLEND ? kTokens : 1], h[GRAD ? kTokens : 1];
+        (void)x;
+        (void)h;
+        const auto load = [&](Walk from, auto &to, uint32_t which) {
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u, from.at += from.step) {
+                to[u] = Four<T>{};
+                if (which >> u & 1)
+                    to[u] = load_four(from.at, n);
+            }
+        };
+        load(walk(p->gate, c, t0), g, in);
+        load(walk(GRAD ? p->dout : p->x, c, t0), d, in);
+        if constexpr (GRAD) {
+            if constexpr (BLEND)
+                load(walk(p->x, c, t0), x, in);
+            load(walk(p->h, c, t0 - 1), h, in & ~firsts);
+        }
         float A[4], H[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -490,11 +534,10 @@ struct GateTile {
         }
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
-            const int64_t t = token(part * kTokens + u);
             if (!(in >> u & 1))
                 continue;
             if (resets >> u & 1)
-                state_of(GRAD ? p->last : p->first, GRAD ? last_at(line, t) : first_at(line, t), H);
+                state_at(entering, marks, u, H);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const Gate w = gate_of<FORM, FINE>(g[u].get(e));
@@ -518,54 +561,53 @@ struct GateTile {
         __syncthreads();
         const uint32_t anew = parts_anew();
         if (threadIdx.x < 64)
-            carry(line, kParts, anew);
+            carry(kParts, anew);
         __syncthreads();
+        if (n == 0)
+            return;
         const bool started = (anew & ((1u << part) - 1)) != 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             H[e] = started ? s.h[part][c + e] : __builtin_fmaf(s.a[part][c + e], s.carry[c + e], s.h[part][c + e]);
+        T *to = out_row(0, t0) + c, *to1 = out_row(GRAD ? 1 : 0, t0) + c;
+        const int64_t step = GRAD ? -p->out_tok[0] : p->out_tok[0], step1 = GRAD ? -p->out_tok[1] : 0;
 #pragma unroll
-        for (int u = 0; u < kTokens; ++u) {
-            const int64_t t = token(part * kTokens + u);
-            if (!(in >> u & 1)) {
-                clear(line, t, c, n);
+        for (int u = 0; u < kTokens; ++u, to += step, to1 += step1) {
+            float out[2][4] = {}, before[4];
+            if (in >> u & 1) {
+                if (resets >> u & 1)
+                    state_at(entering, marks, u, H);
+                if constexpr (GRAD) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        before[e] = h[u].get(e);
+                    if (firsts >> u & 1)
+                        state_at(p->first, s.first, u, before);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Gate w = gate_of<FORM, FINE>(g[u].get(e));
+                    const float v = d[u].get(e);
+                    if constexpr (GRAD)
+                        H[e] = grad_of(w, v + H[e], before[e], BLEND ? x[BLEND ? u : 0].get(e) : 0.f, &out[0][e],
+                                       &out[1][e]);
+                    else
+                        out[0][e] = H[e] = __builtin_fmaf(w.a, H[e], BLEND ? w.rest * v : v);
+                }
+                if (p->state_out && ((GRAD ? firsts : lasts) >> u & 1))
+                    store_four(p->state_out + place_of(GRAD ? s.first : s.last, u), Four<float>::of(H), n);
+            } else if (!past_end(index(u))) {
                 continue;
             }
-            if (resets >> u & 1)
-                state_of(GRAD ? p->last : p->first, GRAD ? last_at(line, t) : first_at(line, t), H);
-            float out[2][4], before[4];
-            if constexpr (GRAD) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    before[e] = h[u].get(e);
-                if (firsts >> u & 1)
-                    state_of(p->first, first_at(line, t), before);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Gate w = gate_of<FORM, FINE>(g[u].get(e));
-                const float v = d[u].get(e);
-                if constexpr (GRAD)
-                    H[e] = grad_of(w, v + H[e], before[e], BLEND ? x[u].get(e) : 0.f, &out[0][e], &out[1][e]);
-                else
-                    out[0][e] = H[e] = __builtin_fmaf(w.a, H[e], BLEND ? w.rest * v : v);
-            }
-            store_four(out_row(0, line, t) + c, Four<T>::of(out[0]), n);
+            store_four(to, Four<T>::of(out[0]), n);
             if constexpr (GRAD)
-                store_four(out_row(1, line, t) + c, Four<T>::of(out[1]), n);
-            if (p->state_out && ((GRAD ? firsts : lasts) >> u & 1))
-                store_piece<float>(p->state_out + (GRAD ? first_at(line, t) : last_at(line, t)) * (int64_t)p->width +
-                                       (int64_t)at, Unpack<float>::pack(H), n);
+                store_four(to1, Four<T>::of(out[1]), n);
         }
     }
-    // Rows that are in no sequence.
-    __device__ __forceinline__ void clear(uint32_t line, int64_t t, int c, int n) const
+    // Whether a place's row is in no sequence and to be cleared.
+    __device__ __forceinline__ bool past_end(int index) const
     {
-        if (p->clear && n > 0 && t >= (int64_t)end && t < (int64_t)p->tokens) {
-            store_four(out_row(0, line, t) + c, Four<T>{}, n);
-            if (GRAD)
-                store_four(out_row(1, line, t) + c, Four<T>{}, n);
-        }
+        return p->clear && low + index >= (int64_t)end && low + index < (int64_t)p->tokens;
     }
     __device__ __forceinline__ uint32_t parts_anew() const
     {
@@ -576,24 +618,30 @@ struct GateTile {
     // A tile without tokens: none with any looks back to it.  Equal sequences of
     // no tokens pass their states through.
     __device__ __forceinline__ bool idle() const { return (low > 0 ? low : 0) >= (int64_t)end; }
-    __device__ __forceinline__ void stream_idle(uint32_t line) const
+    __device__ __forceinline__ void stream_idle() const
     {
-        const int part = threadIdx.x / (C / 4);
+        const int part = tid / (C / 4);
         int c, n;
-        four_of(line, &c, &n);
-        const uint64_t at = column(line) + c;
-        for (int u = 0; u < kTokens; ++u)
-            clear(line, token(part * kTokens + u), c, n);
+        four_of(&c, &n);
+        if (n == 0)
+            return;
+        for (int i = part * kTokens; i < (part + 1) * kTokens; ++i) {
+            if (past_end(i)) {
+                store_four(out_row(0, low + i) + c, Four<T>{}, n);
+                if (GRAD)
+                    store_four(out_row(1, low + i) + c, Four<T>{}, n);
+            }
+        }
         if (!p->ends && p->state_out && part == 0) {
             const float *const from = GRAD ? p->last : p->first;
-            const uint64_t of = (line / p->blocks) * p->width + at;
-            store_piece<float>(p->state_out + of, from ? load_piece<float>(from + of, n) : piece_t{0, 0, 0, 0}, n);
+            const uint64_t of = (line / p->blocks) * p->width + column() + c;
+            store_four(p->state_out + of, from ? load_four(from + of, n) : Four<float>{}, n);
         }
     }
 
     // 2., by one wave: the groups' pairs, the tile's carry.  anew: the groups in
     // which the sweep starts anew, a bit each.
-    __device__ __forceinline__ void carry(uint32_t line, int groups, uint32_t anew)
+    __device__ __forceinline__ void carry(int groups, uint32_t anew)
     {
         const uint32_t tag = __builtin_amdgcn_readfirstlane(s.tag);
         const int lane = threadIdx.x % 64;
@@ -604,7 +652,9 @@ struct GateTile {
         const uint32_t k0 = GRAD && p->ends ? (uint32_t)((p->tokens - end) / TT) : 0;
         // The nearest tiles' words: asked for before the groups are chained, as
         // mostly a tile shortly before is through by then.
-        const Window<4> w = window<4>(line, k0, lane);
+        Window<4> w;
+        if (k > k0)
+            w = window<4>(k0, lane);
         float in = 0.f, a = 1.f, h = 0.f;
         // (Eight at a time: one by one each read of LDS waits for the write before it.)
         for (int g0 = 0; g0 < groups; g0 += 8) {
@@ -644,27 +694,27 @@ struct GateTile {
                 send(mine + C, tag | kStatusAgg, h);
             }
             for (;;) {
-                if (p->far ? nearest(window<kGateWindow>(line, k0, lane), tag, &in)
-                           : nearest(window<4>(line, k0, lane), tag, &in))
+                if (p->far ? nearest(window<kGateWindow>(k0, lane), tag, &in)
+                           : nearest(window<4>(k0, lane), tag, &in))
                     break;
             }
             if (anew == 0)
                 send(mine + C, tag | kStatusPrefix, __builtin_fmaf(a, in, h));
         } else if (p->tiles > 1) {
             if (k <= k0)
-                in = entering(line, lane);
+                in = entering(lane);
             send(mine + C, tag | kStatusPrefix, anew != 0 ? h : __builtin_fmaf(a, in, h));
         } else {
-            in = entering(line, lane);
+            in = entering(lane);
         }
         s.carry[lane] = in;
     }
 
     // What enters the first tile of equal sequences.
-    __device__ __forceinline__ float entering(uint32_t line, int lane) const
+    __device__ __forceinline__ float entering(int lane) const
     {
         const float *const state = GRAD ? p->last : p->first;
-        const uint64_t c = column(line) + lane;
+        const uint64_t c = column() + lane;
         return !p->ends && state && c < p->width ? state[(line / p->blocks) * p->width + c] : 0.f;
     }
 
@@ -674,14 +724,14 @@ struct GateTile {
         uint64_t a[N], h[N];
     };
     template <int N>
-    __device__ __forceinline__ Window<N> window(uint32_t line, uint32_t k0, int lane) const
+    __device__ __forceinline__ Window<N> window(uint32_t k0, int lane) const
     {
         Window<N> w;
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const uint32_t tile = k > k0 + u ? k - 1 - u : k0;
-            w.h[u] = fetch(line, tile, 1, lane);
-            w.a[u] = fetch(line, tile, 0, lane);
+            w.h[u] = fetch(tile, 1, lane);
+            w.a[u] = fetch(tile, 0, lane);
         }
         return w;
     }
@@ -713,7 +763,7 @@ struct GateTile {
         __hip_atomic_store(to, (uint64_t)head << 32 | __builtin_bit_cast(uint32_t, v), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
     }
-    __device__ __forceinline__ uint64_t fetch(uint32_t line, uint32_t tile, int half, int lane) const
+    __device__ __forceinline__ uint64_t fetch(uint32_t tile, int half, int lane) const
     {
         return __hip_atomic_load(p->desc + ((uint64_t)(tile * p->chains + line) * 2 + half) * C + lane,
                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -732,15 +782,19 @@ struct GateTile {
 
     __device__ __forceinline__ void run()
     {
-        if (!(p->ends && mark()) && whole()) {
-            stream_whole();
-            return;
-        }
-        for (uint32_t line = chain; line < chain + count; ++line) {
-            if (idle())
-                stream_idle(line);
+        const bool all = !(p->ends && mark()) && whole();
+#pragma unroll 1
+        for (line = chain; line < chain + count; ++line) {
+            // Arguments and thread are read anew for each line: what is made of
+            // them is kept from one to the next otherwise, and spills.
+            tid = threadIdx.x;
+            asm volatile("" : "+s"(p), "+v"(tid));
+            if (all)
+                stream_whole();
+            else if (idle())
+                stream_idle();
             else
-                stream_any(line);
+                stream_any();
         }
     }
 };
