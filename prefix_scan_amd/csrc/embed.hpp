@@ -59,8 +59,7 @@ struct EmbedGradArgs {
     uint32_t *totals;
     float *partial;                       // [chunks][2][width]
     uint32_t chunk, chunks;
-    int lanes;
-    uint32_t across;
+    uint32_t across;                      // waves along a row
 };
 size_t embed_grad_body_bytes(uint64_t tokens, uint64_t rows, uint64_t width);
 hipError_t launch_embed_grad(EmbedGradArgs a, void *body, hipStream_t stream);

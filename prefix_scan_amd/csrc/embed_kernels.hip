@@ -110,6 +110,15 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(EmbedRowsArgs p)
 // The sort: stable, by digits from the lowest, of (key, position)
 // --------------------------------------------------------------------------
 
+constexpr uint32_t kFewTiles = 8;         // whose keys each workgroup counts itself
+
+// Parts of the table's gradient that the sort's kernels clear: each pass one,
+// the counting before them, whose own work is short, the rest.
+__device__ __forceinline__ int fill_parts(const EmbedGradArgs &p)
+{
+    return p.sort.tiles <= kFewTiles ? p.sort.passes : kSortMaxPasses + 1;
+}
+
 // A token's key: its row, or `rows` for an id that is no row, which comes last.
 __device__ __forceinline__ uint32_t key_at(const EmbedGradArgs &p, uint32_t i)
 {
@@ -117,32 +126,36 @@ __device__ __forceinline__ uint32_t key_at(const EmbedGradArgs &p, uint32_t i)
     return id >= 0 && (uint64_t)id < p.rows ? (uint32_t)id : (uint32_t)p.rows;
 }
 
-// Zeros in the `part`-th of `parts` of the table's gradient, by `count`
-// workgroups of which this is number i.
+// Zeros in the table's gradient, from the `from`-th of `parts` equal parts up to
+// the `to`-th, by `count` workgroups of which this is number i.
 template <class O>
-__device__ void fill_rows(const EmbedGradArgs &p, int part, int parts, uint32_t i, uint32_t count)
+__device__ void fill_rows(const EmbedGradArgs &p, int from, int to, int parts, uint32_t i, uint32_t count)
 {
     const piece_t none = {0, 0, 0, 0};
     constexpr int V = kPiece<O>;
     const bool dense = p.dweight_stride == (int64_t)p.width;
     const uint64_t rows = dense ? 1 : p.rows, width = dense ? p.rows * p.width : p.width;
     const uint64_t units = (width + V - 1) / V, all = rows * units;
-    const uint64_t lo = all / parts * part, hi = part == parts - 1 ? all : all / parts * (part + 1);
+    const uint64_t lo = all / parts * from, hi = to == parts ? all : all / parts * to;
     for (uint64_t u = lo + (uint64_t)i * blockDim.x + threadIdx.x; u < hi; u += (uint64_t)count * blockDim.x) {
         const uint64_t r = dense ? 0 : u / units, c = (dense ? u : u % units) * V;
-        store_piece<O>(static_cast<O *>(p.dweight) + (int64_t)r * p.dweight_stride + c, none,
-                       width - c < (uint64_t)V ? (int)(width - c) : V);
+        O *const to = static_cast<O *>(p.dweight) + (int64_t)r * p.dweight_stride + c;
+        if (width - c >= (uint64_t)V)
+            store_piece_past(to, none);
+        else
+            store_piece<O>(to, none, (int)(width - c));
     }
 }
 
 // How many keys of each tile have each value of the first digit, and zeros
 // where the later digits' are counted.
 template <class O>
-__global__ __launch_bounds__(kSortThreads) void embed_hist_kernel(EmbedGradArgs p, int parts)
+__global__ __launch_bounds__(kSortThreads) void embed_hist_kernel(EmbedGradArgs p)
 {
     __shared__ uint32_t s_bin[kSortBins];
     if (blockIdx.x >= p.sort.tiles) {
-        fill_rows<O>(p, 0, parts, blockIdx.x - p.sort.tiles, gridDim.x - p.sort.tiles);
+        const int parts = fill_parts(p);
+        fill_rows<O>(p, 0, parts - p.sort.passes, parts, blockIdx.x - p.sort.tiles, gridDim.x - p.sort.tiles);
         return;
     }
     const uint32_t tile = blockIdx.x, bins = 1u << p.sort.bits;
@@ -206,13 +219,17 @@ __device__ __forceinline__ void scan_bins(uint32_t *s_bin, uint32_t *s_wave)
 struct SortShared {
     uint32_t bin[kSortBins];                              // counts, then where a digit's keys of the tile go
     uint32_t count[kSortThreads / 64][kSortBins];         // of each wave
+    uint32_t before[kSortBins], others[kSortBins];        // of the tiles before, of all others (few tiles)
     uint32_t wave[kSortThreads / 64];
 };
 
 // One pass over one tile.  Each wave has a contiguous part of it, 64 keys at a
 // time: lanes of one digit find each other by its bits, the lowest adds them
-// up, and so a key's rank is the sum over the keys before it.
-__device__ void sort_tile(const EmbedGradArgs &p, SortShared &s, int pass, uint32_t tile, bool alone)
+// up, and so a key's rank is the sum over the keys before it.  Of few tiles
+// each counts the others' keys itself: counted for it by those that move them
+// they cost an atomic each, which are served one after another from a line of
+// memory (9001 keys: 12 us of the pass's 22).
+__device__ void sort_tile(const EmbedGradArgs &p, SortShared &s, int pass, uint32_t tile)
 {
     constexpr int kRounds = kSortTile / kSortThreads;
     const uint32_t bins = 1u << p.sort.bits, shift = pass * p.sort.bits, lane = threadIdx.x % 64,
@@ -220,8 +237,10 @@ __device__ void sort_tile(const EmbedGradArgs &p, SortShared &s, int pass, uint3
     const int from = (p.sort.passes - pass) & 1;          // the last pass writes [0]
     const uint32_t first = tile * kSortTile + wave * (kRounds * 64) + lane;
     uint32_t key[kRounds], at[kRounds], rank[kRounds];
+    const bool few = p.sort.tiles <= kFewTiles;
     for (uint32_t w = 0; w < kSortThreads / 64; ++w)
         s.count[w][threadIdx.x] = 0;
+    s.before[threadIdx.x] = s.others[threadIdx.x] = 0;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const uint32_t i = first + r * 64;
@@ -234,6 +253,20 @@ __device__ void sort_tile(const EmbedGradArgs &p, SortShared &s, int pass, uint3
         }
     }
     __syncthreads();
+    for (uint32_t other = 0; few && other < p.sort.tiles; ++other) {
+        if (other == tile)
+            continue;
+        uint32_t k[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const uint32_t i = other * kSortTile + r * kSortThreads + threadIdx.x;
+            k[r] = i >= p.tokens ? 0 : pass == 0 ? key_at(p, i) : p.keys[from][i];
+        }
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (other * kSortTile + r * kSortThreads + threadIdx.x < p.tokens)
+                atomicAdd(&(other < tile ? s.before : s.others)[k[r] >> shift & (bins - 1)], 1u);
+    }
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const bool in = first + r * 64 < p.tokens;
@@ -256,7 +289,9 @@ __device__ void sort_tile(const EmbedGradArgs &p, SortShared &s, int pass, uint3
     {
         const uint32_t b = threadIdx.x;
         uint32_t all = 0, before = 0;
-        if (alone) {
+        if (few) {
+            before = s.before[b];
+            all = before + s.others[b];
             for (int w = 0; w < kSortThreads / 64; ++w)
                 all += s.count[w][b];
         } else if (b < bins) {
@@ -291,19 +326,21 @@ __device__ void sort_tile(const EmbedGradArgs &p, SortShared &s, int pass, uint3
         const uint32_t to = s.count[wave][key[r] >> shift & (bins - 1)] + rank[r];
         p.keys[from ^ 1][to] = key[r];
         p.at[from ^ 1][to] = at[r];
-        if (!alone && pass + 1 < p.sort.passes)
+        if (!few && pass + 1 < p.sort.passes)
             atomicAdd(&next[(uint64_t)(to / kSortTile) * bins + (key[r] >> (shift + p.sort.bits) & (bins - 1))], 1u);
     }
 }
 
 template <class O>
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGradArgs p, int pass, int parts)
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGradArgs p, int pass)
 {
     __shared__ SortShared s;
-    if (blockIdx.x >= p.sort.tiles)
-        fill_rows<O>(p, pass + 1, parts, blockIdx.x - p.sort.tiles, gridDim.x - p.sort.tiles);
-    else
-        sort_tile(p, s, pass, blockIdx.x, false);
+    if (blockIdx.x >= p.sort.tiles) {
+        const int parts = fill_parts(p), part = parts - p.sort.passes + pass;
+        fill_rows<O>(p, part, part + 1, parts, blockIdx.x - p.sort.tiles, gridDim.x - p.sort.tiles);
+    } else {
+        sort_tile(p, s, pass, blockIdx.x);
+    }
 }
 
 // All passes over a list of one tile.
@@ -312,11 +349,11 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_one_kernel(EmbedGradA
 {
     __shared__ SortShared s;
     if (blockIdx.x != 0) {
-        fill_rows<O>(p, 0, 1, blockIdx.x - 1, gridDim.x - 1);
+        fill_rows<O>(p, 0, 1, 1, blockIdx.x - 1, gridDim.x - 1);
         return;
     }
     for (int pass = 0; pass < p.sort.passes; ++pass) {
-        sort_tile(p, s, pass, 0, true);
+        sort_tile(p, s, pass, 0);
         __threadfence_block();
         __syncthreads();
     }
@@ -326,71 +363,99 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_one_kernel(EmbedGradA
 // Sums of the sorted list's rows
 // --------------------------------------------------------------------------
 
-template <class O>
-__device__ __forceinline__ void put_row(const EmbedGradArgs &p, uint32_t row, uint64_t c, int n, float (&sum)[8])
+constexpr int kSumBatch = 16;
+
+// N elements of a row, the first n of them.
+template <int N, class O>
+__device__ __forceinline__ void load_some(const O *at, int n, float (&f)[N])
 {
-    O *const at = static_cast<O *>(p.dweight) + (int64_t)row * p.dweight_stride + c;
-    float old[8];
-    if (p.accumulate)
-        load8(at, n, old);
+    if constexpr (N == 8) {
+        load8(at, n, f);
+    } else {
+        const Four<O> x = load_four(at, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        sum[e] = p.accumulate ? __builtin_fmaf(p.scale, sum[e], old[e]) : p.scale * sum[e];
-    store8(at, n, sum);
+        for (int e = 0; e < N; ++e)
+            f[e] = x.get(e);
+    }
+}
+template <int N, class O>
+__device__ __forceinline__ void store_some(O *at, int n, const float (&f)[N])
+{
+    if constexpr (N == 8)
+        store8(at, n, f);
+    else
+        store_four(at, Four<O>::of(f), n);
 }
 
-// One chunk of the sorted list by the lanes of a row: runs that lie within it
-// are done, what it holds of others goes to its partial rows -- 0 of the run
-// that comes from the chunks before, 1 of the one that starts here and goes on.
-// Bound: memory, the rows' bytes; kBatch rows of a thread are under way at once.
+template <class O, int N>
+__device__ __forceinline__ void put_row(const EmbedGradArgs &p, uint32_t row, uint64_t c, int n, float (&sum)[N])
+{
+    O *const at = static_cast<O *>(p.dweight) + (int64_t)row * p.dweight_stride + c;
+    float old[N];
+    if (p.accumulate)
+        load_some<N>(at, n, old);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        sum[e] = p.accumulate ? __builtin_fmaf(p.scale, sum[e], old[e]) : p.scale * sum[e];
+    store_some<N>(at, n, sum);
+}
+
+// One chunk of the sorted list, 64 pieces of its rows, by a wave: runs that lie
+// within it are done, what it holds of others goes to its partial rows -- 0 of
+// the run that comes from the chunks before, 1 of the one that starts here and
+// goes on.
+// Bound: memory, the rows' bytes.  The rows of kSumBatch entries are under way
+// at once, and a chunk is as few entries where that leaves waves enough: keys
+// are the same in all lanes, so that a run's end costs a scalar branch.
 template <class T, class O>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs p)
 {
-    constexpr int kBatch = 8;
-    const int per = 256 / p.lanes;
-    const uint64_t blocks = (uint64_t)((p.chunks + per - 1) / per) * p.across;
-    for (uint64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const uint64_t c = ((b % p.across) * p.lanes + threadIdx.x % p.lanes) * 8;
-        const uint32_t chunk = (uint32_t)(b / p.across) * per + threadIdx.x / p.lanes;
-        if (c >= p.width || chunk >= p.chunks)
-            continue;
-        const int n = p.width - c < 8 ? (int)(p.width - c) : 8;
+    constexpr int V = kPiece<T>;
+    const uint32_t lane = threadIdx.x % 64;
+    const uint64_t waves = (uint64_t)p.chunks * p.across;
+    for (uint64_t w = (uint64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < waves;
+         w += (uint64_t)gridDim.x * 4) {
+        const uint32_t chunk = (uint32_t)(w / p.across);
+        const uint64_t c = ((w % p.across) * 64 + lane) * V;
+        const int n = c >= p.width ? 0 : p.width - c < (uint64_t)V ? (int)(p.width - c) : V;
         const uint32_t lo = chunk * p.chunk, hi = p.tokens - lo < p.chunk ? p.tokens : lo + p.chunk;
-        uint32_t cur = p.keys[0][lo];
-        bool started = lo == 0 || p.keys[0][lo - 1] != cur;
-        float sum[8];
+        const auto entry = [&](uint32_t i0) { return i0 + lane < hi ? i0 + lane : hi - 1; };
+        uint32_t keys = p.keys[0][entry(lo)], ats = p.at[0][entry(lo)];
+        const uint32_t before = lo ? p.keys[0][lo - 1] : ~0u, after = hi < p.tokens ? p.keys[0][hi] : ~0u;
+        uint32_t cur = __builtin_amdgcn_readfirstlane(keys);
+        bool started = before != cur;
+        float sum[V];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < V; ++e)
             sum[e] = 0.f;
         const auto flush = [&](bool ended) {
-            if (cur >= p.rows)
+            if (cur >= p.rows || n == 0)
                 return;
             if (started && ended) {
                 put_row<O>(p, cur, c, n, sum);
             } else {
                 float *const to = p.partial + ((uint64_t)chunk * 2 + (started ? 1 : 0)) * p.width + c;
-                store8(to, n, sum);
+                store_some<V>(to, n, sum);
             }
         };
-        for (uint32_t i0 = lo; i0 < hi; i0 += kBatch) {
-            uint32_t key[kBatch], at[kBatch];
-            float f[kBatch][8];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const uint32_t i = i0 + u < hi ? i0 + u : hi - 1;
-                key[u] = p.keys[0][i];
-                at[u] = p.at[0][i];
+        for (uint32_t i0 = lo; i0 < hi; i0 += kSumBatch) {
+            const uint32_t keys_now = keys, ats_now = ats;
+            if (i0 + kSumBatch < hi) {
+                keys = p.keys[0][entry(i0 + kSumBatch)];
+                ats = p.at[0][entry(i0 + kSumBatch)];
             }
+            uint32_t key[kSumBatch];
+            piece_t raw[kSumBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[u][e] = 0.f;
+            for (int u = 0; u < kSumBatch; ++u) {
+                key[u] = __builtin_amdgcn_readlane(keys_now, u);
+                const uint32_t at = __builtin_amdgcn_readlane(ats_now, u);
+                raw[u] = piece_t{0, 0, 0, 0};
                 if (i0 + u < hi && key[u] < p.rows)
-                    load8(static_cast<const T *>(p.dout) + (int64_t)at[u] * p.dout_stride + c, n, f[u]);
+                    raw[u] = load_piece<T>(static_cast<const T *>(p.dout) + (int64_t)at * p.dout_stride + c, n);
             }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
+            for (int u = 0; u < kSumBatch; ++u) {
                 if (i0 + u >= hi)
                     continue;
                 if (key[u] != cur) {
@@ -398,66 +463,78 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs p)
                     cur = key[u];
                     started = true;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < V; ++e)
                         sum[e] = 0.f;
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum[e] += f[u][e];
+                for (int e = 0; e < V; ++e)
+                    sum[e] += Unpack<T>::get(raw[u], e);
             }
         }
-        flush(hi == p.tokens || p.keys[0][hi] != cur);
+        flush(after != cur);
     }
 }
 
 // The runs that chunks share: where one starts, its partial rows are added, in
-// eight parts one after another and these in their order.
+// eight parts one after another and these in their order.  A workgroup looks at
+// kJoinChunks chunks, 256 columns of their rows.
+constexpr int kJoinChunks = 4;
+
 template <class O>
 __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGradArgs p)
 {
     __shared__ float s_sum[8][256];
-    const uint32_t across = (uint32_t)((p.width + 255) / 256);
-    const uint64_t blocks = (uint64_t)p.chunks * across;
+    const uint32_t across = (uint32_t)((p.width + 255) / 256), lane = threadIdx.x % 64;
+    const uint64_t blocks = (uint64_t)((p.chunks + kJoinChunks - 1) / kJoinChunks) * across;
     for (uint64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const uint32_t chunk = (uint32_t)(b / across);
-        const uint32_t lo = chunk * p.chunk, hi = p.tokens - lo < p.chunk ? p.tokens : lo + p.chunk;
-        if (hi == p.tokens)
-            continue;
-        const uint32_t key = p.keys[0][hi - 1];
-        if (key >= p.rows || p.keys[0][hi] != key || !(lo == 0 || p.keys[0][lo] != key || p.keys[0][lo - 1] != key))
-            continue;
-        // The last chunk that begins with the key.
-        uint32_t last = chunk + 1, past = p.chunks;
-        while (past - last > 1) {
-            const uint32_t mid = last + (past - last) / 2;
-            if (p.keys[0][mid * p.chunk] == key)
-                last = mid;
-            else
-                past = mid;
+        const uint32_t chunk0 = (uint32_t)(b / across) * kJoinChunks, mine = chunk0 + lane;
+        uint32_t keys = 0;
+        bool shared = false;
+        if (lane < kJoinChunks && mine + 1 < p.chunks) {
+            const uint32_t lo = mine * p.chunk, hi = lo + p.chunk;
+            const uint32_t after = p.keys[0][hi], from = p.keys[0][lo], before = lo ? p.keys[0][lo - 1] : ~0u;
+            keys = p.keys[0][hi - 1];
+            shared = keys < p.rows && after == keys && (from != keys || before != keys);
         }
-        const uint64_t c = (b % across) * 256 + threadIdx.x % 32 * 8;
-        const int n = c < p.width ? (p.width - c < 8 ? (int)(p.width - c) : 8) : 0;
-        const uint32_t part = threadIdx.x / 32, many = last - chunk + 1, each = (many + 7) / 8;
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (uint32_t i = part * each; i < many && i < (part + 1) * each && n > 0; ++i) {
-            float f[8];
-            load8(p.partial + ((uint64_t)(chunk + i) * 2 + (i == 0 ? 1 : 0)) * p.width + c, n, f);
+        // The same in all waves.
+        for (uint64_t left = __ballot(shared); left != 0; left &= left - 1) {
+            const uint32_t which = (uint32_t)__builtin_ctzll(left), chunk = chunk0 + which;
+            const uint32_t key = __builtin_amdgcn_readlane(keys, which);
+            // The last chunk that begins with the key: among the next 64, or by
+            // steps of a 64th of what is left.
+            uint32_t last = chunk + 1, past = p.chunks;
+            for (uint32_t step = 1; past - last > 1; step = (past - last + 63) / 64) {
+                const uint64_t at = last + (uint64_t)(lane + 1) * step;
+                const uint64_t same = __ballot(at < past && p.keys[0][(at < past ? at : last) * p.chunk] == key);
+                const uint32_t more = (uint32_t)__popcll(same) * step;
+                last += more;
+                past = more == 64 * step || past - last < step ? past : last + step;
+            }
+            const uint64_t c = (b % across) * 256 + threadIdx.x % 32 * 8;
+            const int n = c < p.width ? (p.width - c < 8 ? (int)(p.width - c) : 8) : 0;
+            const uint32_t part = threadIdx.x / 32, many = last - chunk + 1, each = (many + 7) / 8;
+            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (uint32_t i = part * each; i < many && i < (part + 1) * each && n > 0; ++i) {
+                float f[8];
+                load8(p.partial + ((uint64_t)(chunk + i) * 2 + (i == 0 ? 1 : 0)) * p.width + c, n, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] += f[e];
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sum[e] += f[e];
-        }
+                s_sum[part][threadIdx.x % 32 * 8 + e] = sum[e];
+            __syncthreads();
+            if (part == 0 && n > 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            s_sum[part][threadIdx.x % 32 * 8 + e] = sum[e];
-        __syncthreads();
-        if (part == 0 && n > 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                for (int i = 1; i < 8; ++i)
-                    sum[e] += s_sum[i][threadIdx.x * 8 + e];
-            put_row<O>(p, key, c, n, sum);
+                for (int e = 0; e < 8; ++e)
+                    for (int i = 1; i < 8; ++i)
+                        sum[e] += s_sum[i][threadIdx.x * 8 + e];
+                put_row<O>(p, key, c, n, sum);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -483,31 +560,31 @@ hipError_t grad_to(const EmbedGradArgs &a, hipStream_t stream)
     if (a.sort.tiles == 1) {
         embed_sort_one_kernel<O><<<1 + fill, kSortThreads, 0, stream>>>(a);
     } else {
-        const int parts = a.sort.passes + 1;
         const uint32_t bins = 1u << a.sort.bits;
-        embed_hist_kernel<O><<<a.sort.tiles + fill, kSortThreads, 0, stream>>>(a, parts);
+        if (a.sort.tiles > kFewTiles)
+            embed_hist_kernel<O><<<a.sort.tiles + fill, kSortThreads, 0, stream>>>(a);
         for (int pass = 0; pass < a.sort.passes; ++pass) {
             if (a.totals)
                 embed_columns_kernel<<<(bins + 63) / 64, 1024, 0, stream>>>(
                     a.hist + (uint64_t)pass * a.sort.tiles * bins, a.totals, a.sort.tiles, bins);
-            embed_sort_kernel<O><<<a.sort.tiles + fill, kSortThreads, 0, stream>>>(a, pass, parts);
+            embed_sort_kernel<O><<<a.sort.tiles + fill, kSortThreads, 0, stream>>>(a, pass);
         }
     }
     if (a.tokens == 0)
         return hipGetLastError();
-    const int per = 256 / a.lanes;
-    const unsigned grid = grid_of((uint64_t)((a.chunks + per - 1) / per) * a.across);
+    const unsigned grid = grid_of(((uint64_t)a.chunks * a.across + 3) / 4);
     switch (a.dtype) {
     case LIBSCAN_F32: embed_sum_kernel<float, O><<<grid, 256, 0, stream>>>(a); break;
     case LIBSCAN_BF16: embed_sum_kernel<__bf16, O><<<grid, 256, 0, stream>>>(a); break;
     default: embed_sum_kernel<_Float16, O><<<grid, 256, 0, stream>>>(a); break;
     }
     if (a.chunks > 1)
-        embed_join_kernel<O><<<grid_of((uint64_t)a.chunks * ((a.width + 255) / 256)), 256, 0, stream>>>(a);
+        embed_join_kernel<O><<<grid_of((uint64_t)((a.chunks + kJoinChunks - 1) / kJoinChunks) *
+                                       ((a.width + 255) / 256)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-constexpr uint32_t kFewTiles = 128;       // whose counts each workgroup adds up by itself
+constexpr uint32_t kSomeTiles = 128;      // whose counts each workgroup adds up by itself
 
 size_t up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
@@ -527,9 +604,8 @@ SortPlan sort_plan(uint64_t tokens, uint64_t rows)
 
 uint32_t embed_chunk(uint64_t tokens)
 {
-    // About 512 chunks, of 8 to 128 tokens.
-    uint32_t e = 8;
-    while (e < 128 && tokens / e > 512)
+    uint32_t e = kSumBatch;
+    while (e < 128 && tokens / e > 2048)
         e *= 2;
     return e;
 }
@@ -558,7 +634,8 @@ hipError_t launch_embed_grad(EmbedGradArgs a, void *body, hipStream_t stream)
     a.sort = sort_plan(a.tokens, a.rows);
     a.chunk = embed_chunk(a.tokens);
     a.chunks = (a.tokens + a.chunk - 1) / a.chunk;
-    row_lanes(a.width, &a.lanes, &a.across);
+    const uint64_t piece = 64 * (a.dtype == LIBSCAN_F32 ? 4 : 8);
+    a.across = (uint32_t)((a.width + piece - 1) / piece);
     uint8_t *at = static_cast<uint8_t *>(body);
     const auto take = [&](size_t bytes) {
         void *p = at;
@@ -571,7 +648,7 @@ hipError_t launch_embed_grad(EmbedGradArgs a, void *body, hipStream_t stream)
     }
     const uint64_t cells = ((uint64_t)a.sort.passes * a.sort.tiles) << a.sort.bits;
     a.hist = static_cast<uint32_t *>(take((cells + (1ull << a.sort.bits)) * 4));
-    a.totals = a.sort.tiles > kFewTiles ? a.hist + cells : nullptr;
+    a.totals = a.sort.tiles > kSomeTiles ? a.hist + cells : nullptr;
     a.partial = static_cast<float *>(take(0));
     switch (a.out_dtype) {
     case LIBSCAN_F32: return grad_to<float>(a, stream);
