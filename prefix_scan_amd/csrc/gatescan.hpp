@@ -54,7 +54,6 @@ struct GateArgs {
     float *state_out;                  // h after the last token; or the gradient of `first`; or null
     uint32_t blocks;                   // tiles along the width
     uint32_t chains, tiles;            // lines of tiles, and the tiles of each
-    uint32_t adjacent, draws;          // tiles side by side that are drawn at once, and how many draws there are
     bool far;                          // a look back spans kGateWindow tiles, else four
     uint64_t *ticket, *desc;           // of the chained carry, where there is more than one tile
 };
@@ -62,8 +61,6 @@ struct GateArgs {
 // Lines of tiles and tiles of each; false where a grid cannot hold them.
 bool gate_grid(int dtype, bool grad, bool packed, uint32_t seqs, uint64_t tokens, uint64_t width,
                uint32_t *blocks, uint32_t *chains, uint32_t *tiles);
-// How many tiles side by side are drawn at once.
-uint32_t gate_adjacent(uint32_t chains, uint32_t tiles);
 // Whether looks back span kGateWindow tiles, not four: a chained value moves so
 // many tiles in the time of a look, about a microsecond.
 bool gate_far(uint32_t chains);

@@ -73,15 +73,6 @@ bool gate_grid(int dtype, bool grad, bool packed, uint32_t seqs, uint64_t tokens
     return true;
 }
 
-uint32_t gate_adjacent(uint32_t chains, uint32_t tiles)
-{
-    const uint64_t all = (uint64_t)chains * tiles;
-    uint32_t n = 1;
-    while (n < 4 && n * 2 <= chains && all / (n * 2) >= 1024)
-        n *= 2;
-    return n;
-}
-
 bool gate_far(uint32_t chains) { return chains < 128; }
 
 size_t gate_desc_bytes(int dtype, uint32_t chains, uint32_t tiles)

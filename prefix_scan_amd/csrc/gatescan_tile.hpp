@@ -11,11 +11,9 @@
 //      store.
 //
 // Bound: memory.  Rows are read and written once (descriptors of the carry
-// add 1.5 KB to a tile of 48 KB and more).  A workgroup draws a few tiles side
-// by side from a ticket (one word's draws are served 12 ns apart, a tile of
-// 48 KB takes 7), in the order of their place in their lines, all lines' first
-// tiles first: a tile waits only on tiles that were drawn before it, by
-// workgroups that work on theirs in that order.
+// add 1.5 KB to a tile of 48 KB and more).  A workgroup draws one tile from a
+// ticket, in the order of their place in their lines, all lines' first tiles
+// first: a tile waits only on tiles that were drawn before it.
 #pragma once
 
 #include "device_common.hpp"
@@ -123,9 +121,8 @@ struct GateTile {
     Args *p;
     Shared &s;
     uint64_t end;                // tokens [0, end) are in sequences
-    uint32_t k, chain, count;    // the workgroup's tiles: of `count` lines from `chain` on
-    uint32_t line, tid;          // the one under way; the thread
-    int64_t low;                 // their lowest token (below 0 where a gradient's last tile reaches past them)
+    uint32_t k, line;            // the tile: its place in its line
+    int64_t low;                 // its lowest token (below 0 where a gradient's last tile reaches past them)
 
     __device__ __forceinline__ GateTile(Shared &shared, uint32_t number) : s(shared)
     {
@@ -135,10 +132,8 @@ struct GateTile {
             const uint64_t last = p->ends[p->seqs - 1];
             end = last < end ? last : end;
         }
-        const uint32_t lines = (p->chains + p->adjacent - 1) / p->adjacent;
-        k = number / lines;
-        chain = number % lines * p->adjacent;
-        count = p->chains - chain < p->adjacent ? p->chains - chain : p->adjacent;
+        k = number / p->chains;
+        line = number % p->chains;
         low = GRAD ? (int64_t)p->tokens - (int64_t)(k + 1) * TT : (int64_t)k * TT;
     }
 
@@ -161,8 +156,8 @@ struct GateTile {
     }
 
     // Where sequences start and end among the tile's tokens, and whether any
-    // does; the states of empty ones are passed through, in the workgroup's
-    // channels, by the tiles at whose tokens they lie.
+    // does; the states of empty ones are passed through by the tiles at whose
+    // tokens they lie.
     __device__ __forceinline__ bool mark()
     {
         const int tid = threadIdx.x;
@@ -197,10 +192,8 @@ struct GateTile {
                 while (empty) {
                     const uint32_t which = q - lane + (uint32_t)__builtin_ctzll(empty);
                     empty &= empty - 1;
-                    // (A packed batch's lines are its blocks.)
-                    const uint64_t past = (uint64_t)(chain + count) * C < p->width ? (uint64_t)(chain + count) * C
-                                                                                   : p->width;
-                    for (uint64_t c = (uint64_t)chain * C + lane; c < past; c += 64)
+                    const uint64_t c = column() + lane;
+                    if (lane < C && c < p->width)
                         p->state_out[which * p->width + c] = from ? from[which * p->width + c] : 0.f;
                 }
             }
@@ -341,7 +334,7 @@ struct GateTile {
 
     __device__ __forceinline__ void stream_whole()
     {
-        const int lane8 = tid % kGateLanes, group = tid / kGateLanes;
+        const int lane8 = threadIdx.x % kGateLanes, group = threadIdx.x / kGateLanes;
         const int64_t first = token(group * R);
         const bool mine = column() + lane8 * V < p->width;
         Pieces x = {};
@@ -445,7 +438,7 @@ struct GateTile {
     {
         const uint64_t rest = p->width - column();
         const int left = rest < (uint64_t)C ? (int)rest : C;
-        *c = tid % (C / 4) * 4;
+        *c = threadIdx.x % (C / 4) * 4;
         *n = *c >= left ? 0 : left < 4 ? left : 4;
         if (*n == 4 && *c > left - 4)
             *c = left - 4;
@@ -464,7 +457,7 @@ struct GateTile {
 
     __device__ __forceinline__ void stream_any()
     {
-        const int part = tid / (C / 4);
+        const int part = threadIdx.x / (C / 4);
         int c, n;
         four_of(&c, &n);
         const int64_t at = (int64_t)column() + c, width = (int64_t)p->width;
@@ -620,7 +613,7 @@ struct GateTile {
     __device__ __forceinline__ bool idle() const { return (low > 0 ? low : 0) >= (int64_t)end; }
     __device__ __forceinline__ void stream_idle() const
     {
-        const int part = tid / (C / 4);
+        const int part = threadIdx.x / (C / 4);
         int c, n;
         four_of(&c, &n);
         if (n == 0)
@@ -782,20 +775,12 @@ struct GateTile {
 
     __device__ __forceinline__ void run()
     {
-        const bool all = !(p->ends && mark()) && whole();
-#pragma unroll 1
-        for (line = chain; line < chain + count; ++line) {
-            // Arguments and thread are read anew for each line: what is made of
-            // them is kept from one to the next otherwise, and spills.
-            tid = threadIdx.x;
-            asm volatile("" : "+s"(p), "+v"(tid));
-            if (all)
-                stream_whole();
-            else if (idle())
-                stream_idle();
-            else
-                stream_any();
-        }
+        if (!(p->ends && mark()) && whole())
+            stream_whole();
+        else if (idle())
+            stream_idle();
+        else
+            stream_any();
     }
 };
 
@@ -807,7 +792,7 @@ __global__ __launch_bounds__(kGateThreads, 4) void gatescan_kernel(GateArgs p)
     uint32_t number = blockIdx.x;                    // lines of one tile wait for nothing
     if (p.tiles > 1) {
         if (threadIdx.x == 0) {
-            const TileTicket t = draw_ticket(p.ticket, p.draws);
+            const TileTicket t = draw_ticket(p.ticket, p.chains * p.tiles);
             s.draw = t.tile;
             s.tag = t.tag;
         }
@@ -823,9 +808,9 @@ hipError_t launch_gate_tiles(const GateArgs &a, hipStream_t stream)
 #define LIBSCAN_GATE(FORM)                                                                        \
     if (a.form == FORM) {                                                                         \
         if (a.blend)                                                                              \
-            gatescan_kernel<T, FORM, true, GRAD><<<a.draws, kGateThreads, 0, stream>>>(a);        \
+            gatescan_kernel<T, FORM, true, GRAD><<<a.chains * a.tiles, kGateThreads, 0, stream>>>(a);        \
         else                                                                                      \
-            gatescan_kernel<T, FORM, false, GRAD><<<a.draws, kGateThreads, 0, stream>>>(a);       \
+            gatescan_kernel<T, FORM, false, GRAD><<<a.chains * a.tiles, kGateThreads, 0, stream>>>(a);       \
     }
     LIBSCAN_GATE(GATESCAN_DECAY)
     LIBSCAN_GATE(GATESCAN_LOG)

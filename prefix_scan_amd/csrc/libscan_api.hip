@@ -449,9 +449,7 @@ int gate_prepare(const gatescan_shape_t &s, bool grad, void *scratch, size_t scr
     if (!gate_grid(s.dtype, grad, s.ends != nullptr, s.seqs, s.tokens, s.width, &a->blocks, &a->chains,
                    &a->tiles))
         return LIBSCAN_ERR_SIZE;
-    a->adjacent = gate_adjacent(a->chains, a->tiles);
     a->far = gate_far(a->chains);
-    a->draws = (a->chains + a->adjacent - 1) / a->adjacent * a->tiles;
     const size_t body = gate_desc_bytes(s.dtype, a->chains, a->tiles);
     Scratch scr;
     if (!carve(scratch, scratch_bytes, body, &scr))
