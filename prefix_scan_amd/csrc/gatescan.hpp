@@ -30,6 +30,15 @@ constexpr int kGateThreads = 256;
 constexpr int kGateWindow = 12;        // tiles that a look back spans at most
 constexpr int kGateGroups = kGateThreads / kGateLanes;
 
+// Counters that tiles are drawn from, one for each die, 128 bytes apart: set i
+// has the lines from gate_set(lines, i) on.
+constexpr uint32_t kGateSets = 8, kGateCounterStride = 16;
+constexpr size_t kGateCounterBytes = kGateSets * kGateCounterStride * sizeof(uint64_t);
+__host__ __device__ constexpr uint32_t gate_set(uint32_t lines, uint32_t i)
+{
+    return (uint32_t)((uint64_t)lines * i / kGateSets);
+}
+
 // Tokens of a thread, and of a tile.
 constexpr int gate_rows(int dtype, bool grad) { return dtype == LIBSCAN_F32 && !grad ? 8 : 4; }
 constexpr int gate_tile(int dtype, bool grad) { return kGateGroups * gate_rows(dtype, grad); }
@@ -55,7 +64,10 @@ struct GateArgs {
     uint32_t blocks;                   // tiles along the width
     uint32_t chains, tiles;            // lines of tiles, and the tiles of each
     bool far;                          // a look back spans kGateWindow tiles, else four
-    uint64_t *ticket, *desc;           // of the chained carry, where there is more than one tile
+    // Of the chained carry, where there is more than one tile: this launch's tag
+    // of its words.
+    uint32_t tag;
+    uint64_t *counters, *desc;
 };
 
 // Lines of tiles and tiles of each; false where a grid cannot hold them.

@@ -77,7 +77,7 @@ bool gate_far(uint32_t chains) { return chains < 128; }
 
 size_t gate_desc_bytes(int dtype, uint32_t chains, uint32_t tiles)
 {
-    return tiles > 1 ? (size_t)chains * tiles * 2 * gate_channels(dtype) * sizeof(uint64_t) : 0;
+    return tiles > 1 ? kGateCounterBytes + (size_t)chains * tiles * 2 * gate_channels(dtype) * sizeof(uint64_t) : 0;
 }
 
 hipError_t launch_gatescan(const GateArgs &a, hipStream_t stream)

@@ -10,10 +10,18 @@
 //   3. the threads go over their tokens once more from what enters them, and
 //      store.
 //
-// Bound: memory.  Rows are read and written once (descriptors of the carry
-// add 1.5 KB to a tile of 48 KB and more).  A workgroup draws one tile from a
-// ticket, in the order of their place in their lines, all lines' first tiles
-// first: a tile waits only on tiles that were drawn before it.
+// Bound: memory, or with few lines the chain of carries.  Rows are read and
+// written once (descriptors of the carry add 1.5 KB to a tile of 48 KB and
+// more).  A workgroup draws one tile, from one of eight counters that each have
+// a share of the lines that lie side by side, in the order of the tiles' place
+// in their lines: a tile waits only on tiles that were drawn before it.  One
+// word's draws are served 12 ns apart, and a tile of 48 KB takes 7: from one
+// ticket 8 x 4096 x 2048 bf16 took 118 us, from eight counters 87, where a copy
+// of the same tiles takes 69 to 78 and the bytes at the card's best rate 60.
+// (With a load before the draw's atomic, a second trip to memory that
+// everything else waits for, 157; with several tiles a draw, one after
+// another, 109, as each waits for the one before.)  131073 x 1024 has 16 lines
+// of 1025 tiles: 234 us, 0.23 us a tile from carry to carry.
 #pragma once
 
 #include "device_common.hpp"
@@ -111,7 +119,7 @@ struct GateTile {
         alignas(16) float carry[C];                  // what enters the tile
         piece_t kept[kStash][64];
         uint32_t reset[kParts];                      // whether the sweep starts anew in a part
-        uint32_t draw, tag, seq;
+        uint32_t k, line, seq;
         int32_t first[TT], last[TT];                 // the sequence that starts / ends at a token, or -1
     };
 
@@ -124,7 +132,7 @@ struct GateTile {
     uint32_t k, line;            // the tile: its place in its line
     int64_t low;                 // its lowest token (below 0 where a gradient's last tile reaches past them)
 
-    __device__ __forceinline__ GateTile(Shared &shared, uint32_t number) : s(shared)
+    __device__ __forceinline__ GateTile(Shared &shared, uint32_t k_, uint32_t line_) : s(shared), k(k_), line(line_)
     {
         p = (Args *)__builtin_amdgcn_kernarg_segment_ptr();
         end = p->tokens;
@@ -132,8 +140,6 @@ struct GateTile {
             const uint64_t last = p->ends[p->seqs - 1];
             end = last < end ? last : end;
         }
-        k = number / p->chains;
-        line = number % p->chains;
         low = GRAD ? (int64_t)p->tokens - (int64_t)(k + 1) * TT : (int64_t)k * TT;
     }
 
@@ -636,7 +642,7 @@ struct GateTile {
     // which the sweep starts anew, a bit each.
     __device__ __forceinline__ void carry(int groups, uint32_t anew)
     {
-        const uint32_t tag = __builtin_amdgcn_readfirstlane(s.tag);
+        const uint32_t tag = p->tag;
         const int lane = threadIdx.x % 64;
         if (lane >= C)
             return;
@@ -784,22 +790,50 @@ struct GateTile {
     }
 };
 
+// The next number of a counter {tag, count}, mostly by one atomic.  One with
+// another launch's tag starts anew.
+__device__ __forceinline__ uint32_t gate_draw(uint64_t *counter, uint32_t tag)
+{
+    uint64_t seen = __hip_atomic_fetch_add(counter, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if ((uint32_t)(seen >> 32) == tag)
+        return (uint32_t)seen;
+    ++seen;
+    while ((uint32_t)(seen >> 32) != tag) {
+        if (__hip_atomic_compare_exchange_strong(counter, &seen, (uint64_t)tag << 32 | 1, __ATOMIC_RELAXED,
+                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+            return 0;
+    }
+    return (uint32_t)__hip_atomic_fetch_add(counter, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 template <class T, int FORM, bool BLEND, bool GRAD>
 __global__ __launch_bounds__(kGateThreads, 4) void gatescan_kernel(GateArgs p)
 {
     typedef GateTile<T, FORM, BLEND, GRAD> Tile;
     __shared__ typename Tile::Shared s;
-    uint32_t number = blockIdx.x;                    // lines of one tile wait for nothing
+    uint32_t k = 0, line = blockIdx.x;               // lines of one tile wait for nothing
     if (p.tiles > 1) {
         if (threadIdx.x == 0) {
-            const TileTicket t = draw_ticket(p.ticket, p.chains * p.tiles);
-            s.draw = t.tile;
-            s.tag = t.tag;
+            // There are as many tiles as workgroups, so one of the counters has one.
+            // (Workgroups go to the dies in turn, and so a die has a counter's lines.)
+            uint32_t set = blockIdx.x % kGateSets;
+            for (;; set = (set + 1) % kGateSets) {
+                const uint32_t from = gate_set(p.chains, set), many = gate_set(p.chains, set + 1) - from;
+                if (many == 0)
+                    continue;
+                const uint32_t n = gate_draw(p.counters + set * kGateCounterStride, p.tag);
+                if (n < many * p.tiles) {
+                    s.k = n / many;
+                    s.line = from + n % many;
+                    break;
+                }
+            }
         }
         __syncthreads();
-        number = __builtin_amdgcn_readfirstlane(s.draw);
+        k = __builtin_amdgcn_readfirstlane(s.k);
+        line = __builtin_amdgcn_readfirstlane(s.line);
     }
-    Tile(s, number).run();
+    Tile(s, k, line).run();
 }
 
 template <class T, bool GRAD>

@@ -75,11 +75,12 @@ hipError_t apply_plan(const Scratch &s, const ClearPlan &p, size_t state, hipStr
     return hipSuccess;
 }
 
+// launch: the call's last launch's number among the buffer's since its state was cleared.
 hipError_t prepare_state(const Scratch &s, int kind, uint64_t sig, size_t state,
-                         uint64_t launches, hipStream_t stream)
+                         uint64_t launches, hipStream_t stream, uint64_t *launch = nullptr)
 {
     const uintptr_t key = (uintptr_t)s.base;
-    const ClearPlan p = g_states.prepare(key, kind, sig, state, launches, stream_capturing(stream));
+    const ClearPlan p = g_states.prepare(key, kind, sig, state, launches, stream_capturing(stream), launch);
     const hipError_t e = apply_plan(s, p, state, stream);
     if (e != hipSuccess)
         g_states.forget(key);
@@ -454,10 +455,16 @@ int gate_prepare(const gatescan_shape_t &s, bool grad, void *scratch, size_t scr
     Scratch scr;
     if (!carve(scratch, scratch_bytes, body, &scr))
         return LIBSCAN_ERR_SCRATCH;
-    a->ticket = scr.ticket();
-    a->desc = scr.desc();
-    // Lines of one tile use no scratch at all.
-    return body ? hip_status(prepare_state(scr, kKindDesc, 0, body, 1, stream)) : LIBSCAN_OK;
+    if (body == 0)            // lines of one tile use no scratch at all
+        return LIBSCAN_OK;
+    a->counters = scr.desc();
+    a->desc = scr.desc() + kGateCounterBytes / sizeof(uint64_t);
+    // The launch's tag: its number among the buffer's launches since its state
+    // was cleared, with a bit set that no epoch of the header's ticket has.
+    uint64_t launch = 0;
+    const hipError_t e = prepare_state(scr, kKindDesc, 0, body, 1, stream, &launch);
+    a->tag = ((uint32_t)launch | (uint32_t)kMaxLaunchesBetweenClears) << 2;
+    return hip_status(e);
 }
 
 }  // namespace

@@ -102,8 +102,9 @@ class StateTable {
 public:
     static constexpr size_t kMaxTracked = 4096;
 
+    // launch: if given, the number of the call's last launch since the last clear.
     ClearPlan prepare(uintptr_t key, int kind, uint64_t sig, size_t state, uint64_t launches,
-                      bool capturing)
+                      bool capturing, uint64_t *launch = nullptr)
     {
         std::lock_guard<std::mutex> lock(mu_);
         if (records_.size() > kMaxTracked)
@@ -118,6 +119,8 @@ public:
         const ClearPlan p = plan_call(prev, captured_.count(key) != 0, kind, sig, state, launches,
                                       &next);
         records_[key] = next;
+        if (launch)
+            *launch = next.launches;
         return p;
     }
 
