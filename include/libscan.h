@@ -1,7 +1,8 @@
 /*
  * libscan.h -- device-wide parallel prefix primitives over 32-bit integers
- * for AMD Instinct MI355X (gfx950), and the scans that language models run on
- * them: linear attention with decay and token sampling.  C ABI.
+ * for AMD Instinct MI355X (gfx950), and what language models run on and
+ * beside them: linear attention with decay, gated recurrences, embedding rows,
+ * penalties on logits and token sampling.  C ABI.
  *
  * Conventions shared by every entry point
  * ---------------------------------------

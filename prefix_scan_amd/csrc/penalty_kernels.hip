@@ -9,13 +9,14 @@
 // the slots' logits and the mask.  Logits that nothing touches go out as they
 // came; in place only what changes is written.
 //
-// Bound: what the row's lists cost, which every workgroup of a row goes through
-// twice, and the instructions that a logit costs besides its way in and out.
-// 256 rows of 150001 bf16 with 3000 tokens, 12 biases and 20 masks: 61 us with
-// 16384 logits a workgroup, 73 with 8192; with 10 tokens and nothing else 42,
-// the copy alone 23.  With a count in LDS for every logit (4096 a workgroup)
-// 82, and with each named logit put in its place among a thread's registers
-// 106: that takes more instructions than a copy's time has.
+// Bound: waiting (69% of the waves' time; vector instructions are 18 of 61 us)
+// for the steps before, which every workgroup of a row goes through with all of
+// the row's lists.  256 rows of 150001 bf16 with 3000 tokens, 12 biases and 20
+// masks: 61 us with 16384 logits a workgroup, 73 with 8192; with 10 tokens and
+// nothing else 42, the copy alone 23.  With 384 slots, so that a compute unit
+// holds four workgroups rather than three, 61 to 64.  With a count in LDS for
+// every logit (4096 a workgroup) 82, and with each named logit put in its place
+// among a thread's registers 106.
 #include "penalty.hpp"
 #include "device_common.hpp"
 #include "rows_io.hpp"
