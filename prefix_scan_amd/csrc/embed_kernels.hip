@@ -407,7 +407,7 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs &p, uint32_t row, ui
 // Bound: memory, the rows' bytes.  The rows of kSumBatch entries are under way
 // at once, and a chunk is as few entries where that leaves waves enough: keys
 // are the same in all lanes, so that a run's end costs a scalar branch.
-template <class T, class O>
+template <class T, class O, bool WHOLE>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs p)
 {
     constexpr int V = kPiece<T>;
@@ -431,11 +431,12 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs p)
         const auto flush = [&](bool ended) {
             if (cur >= p.rows || n == 0)
                 return;
+            const int m = WHOLE ? V : n;
             if (started && ended) {
-                put_row<O>(p, cur, c, n, sum);
+                put_row<O>(p, cur, c, m, sum);
             } else {
                 float *const to = p.partial + ((uint64_t)chunk * 2 + (started ? 1 : 0)) * p.width + c;
-                store_some<V>(to, n, sum);
+                store_some<V>(to, m, sum);
             }
         };
         for (uint32_t i0 = lo; i0 < hi; i0 += kSumBatch) {
@@ -451,8 +452,9 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs p)
                 key[u] = __builtin_amdgcn_readlane(keys_now, u);
                 const uint32_t at = __builtin_amdgcn_readlane(ats_now, u);
                 raw[u] = piece_t{0, 0, 0, 0};
-                if (i0 + u < hi && key[u] < p.rows)
-                    raw[u] = load_piece<T>(static_cast<const T *>(p.dout) + (int64_t)at * p.dout_stride + c, n);
+                if (i0 + u < hi && key[u] < p.rows && (!WHOLE || n != 0))
+                    raw[u] = load_piece<T>(static_cast<const T *>(p.dout) + (int64_t)at * p.dout_stride + c,
+                                           WHOLE ? V : n);
             }
 #pragma unroll
             for (int u = 0; u < kSumBatch; ++u) {
@@ -552,6 +554,17 @@ hipError_t rows_from(const EmbedRowsArgs &a, unsigned grid, hipStream_t stream)
 // Workgroups of a loop over `blocks`: a grid holds fewer than 2^32 threads.
 unsigned grid_of(uint64_t blocks) { return (unsigned)(blocks < (1u << 22) ? blocks : 1u << 22); }
 
+// Rows of whole pieces have a kernel of their own, a third as long, without the
+// cut ones' loads and stores (9001 rows of 520: 9 us rather than 10).
+template <class T, class O>
+void sum_from(const EmbedGradArgs &a, unsigned grid, hipStream_t stream)
+{
+    if (a.width % kPiece<T> == 0)
+        embed_sum_kernel<T, O, true><<<grid, 256, 0, stream>>>(a);
+    else
+        embed_sum_kernel<T, O, false><<<grid, 256, 0, stream>>>(a);
+}
+
 template <class O>
 hipError_t grad_to(const EmbedGradArgs &a, hipStream_t stream)
 {
@@ -574,9 +587,9 @@ hipError_t grad_to(const EmbedGradArgs &a, hipStream_t stream)
         return hipGetLastError();
     const unsigned grid = grid_of(((uint64_t)a.chunks * a.across + 3) / 4);
     switch (a.dtype) {
-    case LIBSCAN_F32: embed_sum_kernel<float, O><<<grid, 256, 0, stream>>>(a); break;
-    case LIBSCAN_BF16: embed_sum_kernel<__bf16, O><<<grid, 256, 0, stream>>>(a); break;
-    default: embed_sum_kernel<_Float16, O><<<grid, 256, 0, stream>>>(a); break;
+    case LIBSCAN_F32: sum_from<float, O>(a, grid, stream); break;
+    case LIBSCAN_BF16: sum_from<__bf16, O>(a, grid, stream); break;
+    default: sum_from<_Float16, O>(a, grid, stream); break;
     }
     if (a.chunks > 1)
         embed_join_kernel<O><<<grid_of((uint64_t)((a.chunks + kJoinChunks - 1) / kJoinChunks) *
