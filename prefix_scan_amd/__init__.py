@@ -1189,6 +1189,8 @@ def gatescan_step(gate, x, state, form="decay", blend=False, slots=None, out=Non
 
 def _spaced(t, name):
     """The stride of t's rows, all of its dimensions but the last taken as one."""
+    if t.numel() == 0:                  # no rows, and strides that say nothing
+        return t.shape[-1]
     stride, count = 0, 1
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
