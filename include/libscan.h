@@ -528,7 +528,8 @@ enum { GATESCAN_DECAY = 0, GATESCAN_LOG = 1, GATESCAN_SIGMOID = 2 };
 
 /* Rows of one tensor: token t of sequence s starts `s * seq_stride + t *
  * token_stride` ELEMENTS after data; the elements of a row are contiguous.
- * data is aligned to its element. */
+ * data is aligned to its element.  An output's rows overlap neither one
+ * another nor an input (in any call below); an input's may. */
 typedef struct {
     void *data;
     int64_t seq_stride, token_stride;
@@ -622,7 +623,8 @@ typedef struct {
  *
  * ids            device, `tokens` int32 or int64.
  * weight, out    device; row i starts i * stride ELEMENTS after the pointer,
- *                which is aligned to its element.  out overlaps no input.
+ *                which is aligned to its element.  out overlaps no input, and
+ *                its rows not one another.
  * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (types, id_bytes, width 0), ERR_SIZE
  * (rows above EMBED_MAX_ROWS, tokens or width above LIBSCAN_MAX_N), ERR_HIP.
  */
@@ -635,7 +637,8 @@ int embed_rows(const embed_shape_t *shape, const void *weight, int64_t weight_st
  * to what dweight holds and rows of no id are left as they are.  Ids outside
  * [0, rows) are passed over and their rows of dout are not read.  The tokens
  * are sorted by their rows (stably) and summed in 32 bits in an order that is
- * the same every time; a row is rounded once.  dweight overlaps no input.
+ * the same every time; a row is rounded once.  dweight overlaps no input, and
+ * its rows not one another.
  * scratch: at least embed_grad_scratch_bytes(shape) bytes.
  * Errors as above; ERR_SIZE also for more than EMBED_MAX_ROWS tokens;
  * ERR_ARG for an accumulate other than 0 and 1; ERR_SCRATCH.

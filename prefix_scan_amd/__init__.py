@@ -10,7 +10,8 @@ PyTorch supplies device memory and streams.  Tensors must be on a CUDA (HIP)
 device, contiguous, with 4-byte elements (torch.int32 or torch.uint32), or
 8-byte elements (torch.int64 or torch.uint64) for the *_u64 entry points.
 Rows of linear attention, gated recurrences, embeddings and logits are float32,
-bfloat16 or float16, with any strides whose last is 1.
+bfloat16 or float16, with any strides whose last is 1; an output's rows may not
+overlap one another.
 """
 import ctypes
 import functools
@@ -823,12 +824,25 @@ def _states(shape, t, name, device, count=None):
         device)
 
 
+def _apart(t, name):
+    """Refuses an output (or None) whose rows share elements, or may: in the order of the strides,
+    each dimension has to step past all that those before it cover."""
+    if t is None or t.numel() == 0:
+        return
+    covered = t.shape[-1]
+    for s, n in sorted((s, n) for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1):
+        if s < covered:
+            raise ValueError("the rows of %s overlap" % name)
+        covered += s * (n - 1)
+
+
 def _out_like(out, name, want, dtype, device):
     """`out`, checked, or None."""
     if out is not None:
         _dev_rows(out, name, dtype, len(want), device)
         if tuple(out.shape) != tuple(want):
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(want), tuple(out.shape)))
+        _apart(out, name)
     return out
 
 
@@ -1090,6 +1104,7 @@ def _gatescan_plan(gate, x, ends, state, out, state_out):
     _given(x, "x")
     _gate_rows(gate, 3 if ends is None else 2, (x, "x"), (out, "out"))
     _gate_states(gate, _gate_ends(gate, ends), (state, "state"), (state_out, "state_out"))
+    _apart(out, "out")
     return _GatePlan(gate, ends, (gate, x, out), False)
 
 
@@ -1123,6 +1138,8 @@ def gatescan(gate, x, form="decay", blend=False, ends=None, state=None, want_sta
 def _gatescan_grad_plan(dout, gate, x, out, ends, state, dstate_out, dgate, dx, dstate):
     _gate_rows(gate, 3 if ends is None else 2, (dout, "dout"), (x, "x"), (out, "out"), (dgate, "dgate"), (dx, "dx"))
     _gate_states(gate, _gate_ends(gate, ends), (state, "state"), (dstate_out, "dstate_out"), (dstate, "dstate"))
+    _apart(dgate, "dgate")
+    _apart(dx, "dx")
     return _GatePlan(gate, ends, (dout, gate, x, out, dgate, dx), True)
 
 
@@ -1161,6 +1178,7 @@ def _gatescan_step_plan(gate, x, state, slots, out, state_out):
     elif pool != gate.shape[0]:
         raise ValueError("without slots, state must hold one state for each of %d rows, got %d"
                          % (gate.shape[0], pool))
+    _apart(out, "out")
     return _GatePlan(gate, None, (gate, x, out), None)
 
 
@@ -1245,6 +1263,7 @@ def _embed_grad_plan(to, dout, ids, dweight):
         _dev_rows(dweight, "dweight", to, 2, dout.device)
         if dweight.shape[1] != dout.shape[-1]:
             raise ValueError("dweight must be %d wide, got %d" % (dout.shape[-1], dweight.shape[1]))
+        _apart(dweight, "dweight")
     return (fields, dout.shape[-1], _spaced(dout, "dout"), dout.shape[-1] if dweight is None else dweight.stride(0),
             to, dout.device, dout.get_device())
 
@@ -1337,8 +1356,6 @@ def _penalize_plan(logits, tokens, ends, prompt, repetition, presence, frequency
     if vocab > SAMPLE_MAX_VOCAB:
         raise ValueError("logits must have at most %d columns, got %d" % (SAMPLE_MAX_VOCAB, vocab))
     _out_like(out, "out", logits.shape, logits.dtype, device)
-    if out is not None and rows > 1 and abs(out.stride(0)) < vocab:
-        raise ValueError("the rows of out overlap")
     past = _lists(tokens, ends, "tokens", rows, device)
     bias = _lists(bias_tokens, bias_ends, "bias_tokens", rows, device)
     if (bias_tokens is None) != (bias_values is None):
