@@ -1407,12 +1407,13 @@ def penalize_logits(logits, tokens=None, ends=None, prompt=None, repetition=1.0,
     of 32 bits [G, ceil(V / 32)], a set bit for each token that may follow;
     row r has mask[mask_slots[r]] (int32 [R], outside as -1: none), mask[r]
     without slots; what is banned gets -inf.  Returns out, which may be
-    logits itself; it carries no gradient."""
+    logits itself; it carries no gradient, and tensors that require one are
+    refused."""
     each = [t if isinstance(t, torch.Tensor) else None for t in (repetition, presence, frequency)]
     fields, stride, out_stride, past, bias, values, mask_stride, masks, dtype, device, index = _planned(
         _penalize_plan, logits, tokens, ends, prompt, *each, bias_tokens, bias_values, bias_ends, mask,
         mask_slots, out)
-    if torch.is_grad_enabled() and logits.requires_grad:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (logits, *each, bias_values)):
         raise RuntimeError("penalize_logits records no gradient: call it under torch.no_grad()")
     if out is None:
         out = _new(fields[1:], dtype, device, stream)
