@@ -565,8 +565,9 @@ typedef struct {
  * finite reaches no earlier token, no other channel and no other sequence.  An
  * infinite h stays infinite while a is not 0.
  * Errors: ERR_NULL, ERR_ALIGN, ERR_ARG (type, form, flags, width 0), ERR_SIZE
- * (2^24 sequences, LIBSCAN_MAX_N tokens or channels, or 2^24 tiles of 128
- * tokens and 64 channels, 32 for f32), ERR_SCRATCH, ERR_HIP.
+ * (more than 2^24 sequences, or LIBSCAN_MAX_N tokens or channels; 2^24 tiles or
+ * more of 128 tokens, 256 in f32's forward pass, by 64 channels, 32 of f32),
+ * ERR_SCRATCH, ERR_HIP.
  */
 size_t gatescan_scratch_bytes(const gatescan_shape_t *shape, int grad);
 int gatescan(const gatescan_shape_t *shape, const gatescan_rows_t *gate, const gatescan_rows_t *x,

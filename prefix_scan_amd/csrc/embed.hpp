@@ -4,7 +4,9 @@
 // (their rows of the table) are sorted stably with their positions, chunks of
 // the sorted list are summed, and what a run of one key left in several chunks
 // is joined.  A run's rows are added in the order of their positions within a
-// chunk, and chunk by chunk, so the bits are the same every time.
+// chunk; of a run in several chunks eight parts, of as many chunks one after
+// another each, are added up in the chunks' order, and then these in theirs.
+// So the bits are the same every time.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,7 +57,7 @@ struct EmbedGradArgs {
     bool accumulate;
     SortPlan sort;
     uint32_t *keys[2], *at[2];            // sorted back and forth; the last pass writes [0]
-    uint32_t *hist;                       // [passes][tiles][bins], then [passes][bins]
+    uint32_t *hist;                       // [passes][tiles][bins], then the current pass's totals [bins]
     uint32_t *totals;
     float *partial;                       // [chunks][2][width]
     uint32_t chunk, chunks;
