@@ -1413,8 +1413,10 @@ def penalize_logits(logits, tokens=None, ends=None, prompt=None, repetition=1.0,
     fields, stride, out_stride, past, bias, values, mask_stride, masks, dtype, device, index = _planned(
         _penalize_plan, logits, tokens, ends, prompt, *each, bias_tokens, bias_values, bias_ends, mask,
         mask_slots, out)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (logits, *each, bias_values)):
-        raise RuntimeError("penalize_logits records no gradient: call it under torch.no_grad()")
+    if torch.is_grad_enabled():
+        for t in (logits, bias_values, *each):
+            if t is not None and t.requires_grad:
+                raise RuntimeError("penalize_logits records no gradient: call it under torch.no_grad()")
     if out is None:
         out = _new(fields[1:], dtype, device, stream)
     a = _Penalty(*fields, logits.data_ptr(), stride, out.data_ptr(), out_stride,
