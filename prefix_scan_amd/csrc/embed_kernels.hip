@@ -110,7 +110,10 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(EmbedRowsArgs p)
 // The sort: stable, by digits from the lowest, of (key, position)
 // --------------------------------------------------------------------------
 
-constexpr uint32_t kFewTiles = 8;         // whose keys each workgroup counts itself
+// Tiles whose keys each workgroup counts itself.  Whole calls (50021 x 64 bf16) with
+// and without that, us: 2 tiles 36 and 53, 4 46 and 68, 8 62 and 85, 12 76 and 93,
+// 16 92 and 98, 25 137 and 110.  (12 and 16 are not counted so all the same.)
+constexpr uint32_t kFewTiles = 8;
 
 // Parts of the table's gradient that the sort's kernels clear: each pass one,
 // the counting before them, whose own work is short, the rest.
@@ -555,7 +558,9 @@ hipError_t rows_from(const EmbedRowsArgs &a, unsigned grid, hipStream_t stream)
 unsigned grid_of(uint64_t blocks) { return (unsigned)(blocks < (1u << 22) ? blocks : 1u << 22); }
 
 // Rows of whole pieces have a kernel of their own, a third as long, without the
-// cut ones' loads and stores (9001 rows of 520: 9 us rather than 10).
+// cut ones' loads and stores.  Whole calls with it and without, us: 500 rows of 520
+// 24.7 and 25.9, 9001 52.8 and 54.5, 32768 f32 rows of 1024 103.0 and 105.3, 65536
+// bf16 ones 136.3 and 136.9.
 template <class T, class O>
 void sum_from(const EmbedGradArgs &a, unsigned grid, hipStream_t stream)
 {
@@ -597,7 +602,11 @@ hipError_t grad_to(const EmbedGradArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-constexpr uint32_t kSomeTiles = 128;      // whose counts each workgroup adds up by itself
+// Tiles whose counts each workgroup adds up by itself, without a kernel between the
+// passes that does.  Whole calls (50021 x 8 bf16) without that kernel and with it,
+// us: 16 tiles 96 and 95, 32 112 and 104, 64 142 and 121, 128 188 and 141, 192 239 and
+// 163, 512 553 and 334: it would be no loss from 16 tiles on.
+constexpr uint32_t kSomeTiles = 128;
 
 size_t up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
@@ -615,6 +624,14 @@ SortPlan sort_plan(uint64_t tokens, uint64_t rows)
     return s;
 }
 
+// As few as leave some 2048 chunks: a chunk is a wave's work from its first entry to
+// its last, and each leaves up to two rows to be joined.  Added to a table of 20011
+// rows (bf16), us by chunks of 16, 32, 64 and 128 entries:
+//      9001 tokens of 520    44   50   62   87
+//     65536                 122  115  120  143
+//    262144                 268  214  190  183
+//     16384 of 2048          68   72   82  110
+//    131072                 316  284  268  266
 uint32_t embed_chunk(uint64_t tokens)
 {
     uint32_t e = kSumBatch;

@@ -73,8 +73,13 @@ struct GateArgs {
 // Lines of tiles and tiles of each; false where a grid cannot hold them.
 bool gate_grid(int dtype, bool grad, bool packed, uint32_t seqs, uint64_t tokens, uint64_t width,
                uint32_t *blocks, uint32_t *chains, uint32_t *tiles);
-// Whether looks back span kGateWindow tiles, not four: a chained value moves so
-// many tiles in the time of a look, about a microsecond.
+// Whether looks back span kGateWindow tiles, not four.  With few lines a chained
+// value moves further in the time of a look than four tiles: lines of 1025 tiles
+// (bf16, log, blend) take with twelve 198 us where there is one, 164 with four and
+// 234 with 16, with four 268, 230 and 282.  The more lines, the more a look's words
+// cost: 2^26 elements in 16 lines take 122 us with twelve and 145 with four, in 32
+// and 48 the same, in 64 to 384 with four 1 to 3% less (92.7 and 89.9 in 128; the
+// gradient 146.5 and 144.2).  From 64 lines to 127 that is given up.
 bool gate_far(uint32_t chains);
 size_t gate_desc_bytes(int dtype, uint32_t chains, uint32_t tiles);
 

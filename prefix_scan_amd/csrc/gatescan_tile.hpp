@@ -20,8 +20,22 @@
 // of the same tiles takes 69 to 78 and the bytes at the card's best rate 60.
 // (With a load before the draw's atomic, a second trip to memory that
 // everything else waits for, 157; with several tiles a draw, one after
-// another, 109, as each waits for the one before.)  131073 x 1024 has 16 lines
-// of 1025 tiles: 234 us, 0.23 us a tile from carry to carry.
+// another, 109, as each waits for the one before.)  A line's carry takes 0.16 us a
+// tile: one to eight lines of 1025 tiles 164 to 198 us.  Of 16 such lines (131073 x
+// 1024) 64 tiles each fit on the card at once, and a tile is there for 15 us from its
+// draw to its last store: 234 us.
+//
+// Both paths are in one kernel, which has the registers of the other path: 128 with
+// 16 spilled (forward, 16 bits), 64 to 87 (f32), 30 to 76 (gradients; log of 16 bits
+// 122, 205 with blend).  The whole tiles' path alone takes 87 to 101 (forward) and
+// 90 to 128 (gradients), of which log with blend of 16 bits spills two or three.
+//
+// Rows of whole tiles are read and written past what the caches keep.  8 x 4096 x
+// 2048 bf16 takes 89 us so, 88 with stores like any others and 99 with loads like
+// any others too, its gradient 151, 136 and 157; with a kernel after it that reads
+// the outputs 132, 127 and 146 (gradient 215, 210 and 215).  32 x 128 x 8192, which
+// the caches hold, 39, 40 and 33, and 63, 60 and 54 with that kernel: there the
+// marks cost more than they save.
 #pragma once
 
 #include "device_common.hpp"
@@ -286,8 +300,8 @@ struct GateTile {
                 }
                 A[e] *= w.a;
             }
-            // Row by row: moved behind all rows' gates, the sums would need more
-            // registers than there are.
+            // Row by row: moved behind all rows' gates, the sums need more registers
+            // (sigmoid with blend of f32 128 with 13 spilled, not 87 and none).
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 asm volatile("" : "+v"(A[e]), "+v"(H[e]));
@@ -413,7 +427,7 @@ struct GateTile {
     }
 
     // What the carrying wave's threads keep of their tile, in LDS while they
-    // carry: their registers are full of it.
+    // carry: kept in registers beside the carry, 14 to 126 of them spill.
     template <class X>
     __device__ __forceinline__ void stash(const X &x) const
     {

@@ -279,6 +279,19 @@ hipError_t run_penalize(const penalty_args_t &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Workgroups of 512 threads and 16384 logits (f32: 8192), or of 256 and 2048 (1024)
+// where the large ones would be fewer than 512, two a compute unit.  Each goes
+// through all of its row's list, so that large ones do less in all; small ones are
+// more, which counts where lists are long and rows few.  bf16, vocabulary of 32000,
+// us by small and by large workgroups, lists of 1000 | of 32768 tokens:
+//     16 rows, 32 large workgroups      7.3  7.4 |   80  186
+//     64 rows, 128                      7.4  7.6 |  153  189
+//    128 rows, 256                     12.6  8.1 |  267  295
+//    192 rows, 384                     14.8  9.1 |  309  299
+//    256 rows, 512                     20.3 10.1 |  449  330
+//   1024 rows, 2048                    72.1 32.4 | 1626  994
+// (f32 and 150001 logits alike.)  Between 256 and 512 short lists would gain by the
+// large ones and long lists of few rows lose.
 template <class T>
 hipError_t size_penalize(const penalty_args_t &a, hipStream_t stream)
 {
