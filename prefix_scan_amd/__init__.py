@@ -825,15 +825,25 @@ def _states(shape, t, name, device, count=None):
 
 
 def _apart(t, name):
-    """Refuses an output (or None) whose rows share elements, or may: in the order of the strides,
-    each dimension has to step past all that those before it cover."""
+    """Refuses an output (or None) whose rows share elements."""
     if t is None or t.numel() == 0:
         return
-    covered = t.shape[-1]
-    for s, n in sorted((s, n) for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1):
+    width = covered = t.shape[-1]
+    steps = sorted((s, n) for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1)
+    for s, n in steps:                  # mostly each steps past all that those before it cover
         if s < covered:
-            raise ValueError("the rows of %s overlap" % name)
+            break
         covered += s * (n - 1)
+    else:
+        return
+    apart = steps[0][0] >= width
+    if apart:                           # woven into each other: by where each row starts
+        at = torch.zeros(1, dtype=torch.int64)
+        for s, n in steps:
+            at = (at.unsqueeze(1) + s * torch.arange(n)).flatten()
+        apart = bool((at.sort().values.diff() >= width).all())
+    if not apart:
+        raise ValueError("the rows of %s overlap" % name)
 
 
 def _out_like(out, name, want, dtype, device):

@@ -1,6 +1,8 @@
 """Outputs whose rows share elements are refused: rows are written by different
 workgroups, in no order.  Inputs may be broadcast.  No GPU: the library is a
 stand-in."""
+import random
+
 import pytest
 import torch
 
@@ -109,3 +111,27 @@ def test_a_width_of_one(ready):
     ps.gatescan(x, x, out=Z(8).as_strided((2, 4, 1), (1, 2, 5)))
     with pytest.raises(ValueError, match="overlap"):
         ps.gatescan(x, x, out=Z(8).as_strided((2, 4, 1), (1, 1, 1)))
+
+
+def test_any_strides():
+    # by the elements themselves, among them rows woven into each other
+    rng, seen = random.Random(5), {True: 0, False: 0}
+    for _ in range(4000):
+        dims = rng.randint(1, 3)
+        shape = tuple(rng.randint(1, 4) for _ in range(dims)) + (rng.randint(1, 5),)
+        t = Z(400).as_strided(shape, tuple(rng.randint(0, 25) for _ in range(dims)) + (1,))
+        shared = shares(t)
+        seen[shared] += 1
+        if shared:
+            with pytest.raises(ValueError, match="overlap"):
+                ps._apart(t, "out")
+        else:
+            ps._apart(t, "out")
+    assert min(seen.values()) > 500
+
+
+def test_rows_that_only_their_starts_show_apart(ready):
+    # 0, 10, 20 and 15, 25, 35
+    out = Z(40).as_strided((2, 3, 5), (15, 10, 1))
+    assert not shares(out)
+    ps.gatescan(Z(2, 3, 5), Z(2, 3, 5), out=out)
