@@ -11,6 +11,7 @@
  *   frees or keeps any of them past the call.  Arrays are dense and
  *   contiguous, element i at byte offset 4*i, and must be 4-byte aligned.
  *   Host pointers are named *_host and are plain host memory.
+ * Device.  A call's memory and its stream are the current device's.
  * Stream.  Every call is ordered on `stream` (NULL is the null stream).  It
  *   enqueues its kernels and returns; it waits for the GPU only when the
  *   caller asks for a result on the host (a non-NULL *_host pointer), because

@@ -6,8 +6,8 @@ same name in ``libscan.so`` (declared in ``include/libscan.h``).  All
 computation runs in the library's HIP kernels; there is no CPU fallback, and
 a missing ``libscan.so`` raises.
 
-PyTorch supplies device memory and streams.  Tensors must be on a CUDA (HIP)
-device, contiguous, with 4-byte elements (torch.int32 or torch.uint32), or
+PyTorch supplies device memory and streams.  Tensors must be on the current CUDA
+(HIP) device, contiguous, with 4-byte elements (torch.int32 or torch.uint32), or
 8-byte elements (torch.int64 or torch.uint64) for the *_u64 entry points.
 Rows of linear attention, gated recurrences, embeddings and logits are float32,
 bfloat16 or float16, with any strides whose last is 1; an output's rows may not
